@@ -52,7 +52,9 @@ STATUS = {0: "ATTN_RES_OK", 1: "ATTN_RES_EINVAL", 2: "ATTN_RES_EALIGN",
 EXPORTS = ("attn_res", "attn_res_status_string", "attn_res_hidden_size",
            "attn_res_max_blocks", "attn_res_launch_shape", "attn_res_device_status",
            "attn_res_selftest_wait_timeout", "attn_res_h", "attn_res_tp_sums",
-           "attn_res_tp_sq", "attn_res_tp_finish", "attn_res_tp_sums_width")
+           "attn_res_tp_sq", "attn_res_tp_finish", "attn_res_tp_sums_width",
+           "attn_res_mx_scale_bytes", "attn_res_mx_quantize", "attn_res_mx_dequantize",
+           "attn_res_mx_norm", "attn_res_mx_matmul")
 
 
 class Layout(ctypes.Structure):
@@ -61,6 +63,13 @@ class Layout(ctypes.Structure):
                 ("blocks_token", ctypes.c_int64), ("blocks_slot", ctypes.c_int64),
                 ("out_row", ctypes.c_int64), ("blocks_capacity", ctypes.c_int32),
                 ("flags", ctypes.c_uint32), ("blocks_group", ctypes.c_int32)]
+
+
+class Mx(ctypes.Structure):
+    """attn_res_mx_t"""
+    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p)]
 
 
 class AttnResError(RuntimeError):
@@ -118,6 +127,17 @@ def lib():
         L.attn_res_tp_finish.restype = ctypes.c_int
         L.attn_res_tp_finish.argtypes = [i64, i64, vp, vp, vp, i32, i32, vp, f32, f32, vp, i64,
                                          vp, vp, i64, lp, vp]
+        mp, u32 = ctypes.POINTER(Mx), ctypes.c_uint32
+        L.attn_res_mx_scale_bytes.restype = i64
+        L.attn_res_mx_scale_bytes.argtypes = [i32, i64, i64]
+        L.attn_res_mx_quantize.restype = ctypes.c_int
+        L.attn_res_mx_quantize.argtypes = [vp, i64, mp, u32, vp]
+        L.attn_res_mx_dequantize.restype = ctypes.c_int
+        L.attn_res_mx_dequantize.argtypes = [mp, vp, i64, u32, vp]
+        L.attn_res_mx_norm.restype = ctypes.c_int
+        L.attn_res_mx_norm.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, mp, u32, vp]
+        L.attn_res_mx_matmul.restype = ctypes.c_int
+        L.attn_res_mx_matmul.argtypes = [mp, mp, vp, i64, u32, vp]
         _lib = L
     return _lib
 

@@ -1,9 +1,11 @@
 """Build ``libattn_res.so`` for sm_103a, in-tree.
 
-Ten translation units: the C ABI (attn_res_api.cu) and the kernel
-specialisations for each num_blocks value (attn_res_inst.cu compiled nine
-times with -DATTN_RES_S=0..8), compiled in parallel and linked into one shared
-object with the CUDA runtime linked statically.
+Twelve translation units: the C ABI (attn_res_api.cu; attn_res_mx_api.cu with
+the microscaled row kernels), the microscaled product (attn_res_mx_product.cu)
+and the mixture's kernel specialisations for each num_blocks value
+(attn_res_inst.cu compiled nine times with -DATTN_RES_S=0..8), compiled in
+parallel and linked into one shared object with the CUDA runtime linked
+statically.
 """
 from __future__ import annotations
 
@@ -39,7 +41,8 @@ def nvcc() -> str:
 def _sources():
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
             if f.endswith((".cu", ".cuh"))] + [os.path.join(INCLUDE, "attn_res.h")]
-    units = [("attn_res_api", os.path.join(CSRC, "attn_res_api.cu"), [])]
+    units = [(n, os.path.join(CSRC, n + ".cu"), [])
+             for n in ("attn_res_mx_product", "attn_res_api", "attn_res_mx_api")]
     for s in range(9):
         units.append((f"attn_res_inst_s{s}", os.path.join(CSRC, "attn_res_inst.cu"),
                       [f"-DATTN_RES_S={s}"]))

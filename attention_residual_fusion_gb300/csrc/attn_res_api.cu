@@ -767,6 +767,11 @@ attn_res_status_t run_tp(int phase, int64_t Hs, int64_t H, attn_res_bf16_t* pref
 
 }  // namespace
 
+namespace attn_res_host {
+attn_res_status_t current_device(int* device) { return check_device(device); }
+cudaError_t device_status_word(int device, unsigned** word) { return status_word(device, word); }
+}  // namespace attn_res_host
+
 extern "C" {
 
 attn_res_status_t attn_res_tp_sums(int64_t Hs, const attn_res_bf16_t* prefix,

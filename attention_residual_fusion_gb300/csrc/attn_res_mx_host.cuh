@@ -1,0 +1,29 @@
+// attn_res_mx_host.cuh -- host side shared by the microscaled entry points.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "attn_res_launch.cuh"
+#include "attn_res_mx_product.cuh"
+
+namespace attn_res_host {
+
+// Defined in attn_res_api.cu: the current device, if it is one the kernels
+// run on, and its status word.
+attn_res_status_t current_device(int* device);
+cudaError_t device_status_word(int device, unsigned** word);
+
+// Defined in attn_res_mx_product.cu: the launch of a checked product.
+struct ProductCall {
+  const attn_res_mx_t* a;
+  const attn_res_mx_t* w;
+  attn_res_bf16_t* out;
+  int64_t out_row;
+  bool pdl;
+  int device;
+  unsigned* err;
+  cudaStream_t stream;
+};
+cudaError_t launch_mx_product(const ProductCall& c);
+
+}  // namespace attn_res_host

@@ -1,0 +1,104 @@
+// attn_res_mx_product.cu -- launches of the microscaled product.
+#include "attn_res_mx_host.cuh"
+
+namespace attn_res_host {
+namespace {
+
+using namespace attn_res_dev;
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_tiled(EncodeTiled* out) {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult state;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                     cudaEnableDefault, &state);
+    if (e != cudaSuccess) return e;
+    if (state != cudaDriverEntryPointSuccess || f == nullptr) return cudaErrorNotSupported;
+    found.store(f, std::memory_order_release);
+  }
+  *out = reinterpret_cast<EncodeTiled>(f);
+  return cudaSuccess;
+}
+
+// Tensor map of an operand's codes as bytes: boxes of 128 bytes x `rows`,
+// 128-byte swizzle; bytes past the row's end and rows past the last read as 0.
+cudaError_t operand_map(const attn_res_mx_t& x, uint32_t rows, CUtensorMap* map) {
+  EncodeTiled enc;
+  cudaError_t e = encode_tiled(&enc);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dim[2] = {(cuuint64_t)(x.cols * mx_bits(x.format) / 8), (cuuint64_t)x.rows};
+  const cuuint64_t stride[1] = {(cuuint64_t)x.row_bytes};
+  const cuuint32_t box[2] = {128, rows};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.data, dim, stride, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int FMT, int TN>
+cudaError_t launch(const ProductCall& c) {
+  using C = ProductCfg<FMT, TN>;
+  void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_kernel<FMT, TN>;
+  static std::atomic<uint64_t> enabled{0};
+  const uint64_t bit = 1ull << c.device;
+  if (!(enabled.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    enabled.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  CUtensorMap map_a, map_w;
+  cudaError_t e = operand_map(*c.a, TN, &map_a);
+  if (e == cudaSuccess) e = operand_map(*c.w, 128, &map_w);
+  if (e != cudaSuccess) return e;
+  ProductParams p = {};
+  p.a_scales = c.a->scales;
+  p.w_scales = c.w->scales;
+  p.a_g = c.a->tensor_scale;
+  p.w_g = c.w->tensor_scale;
+  p.out = c.out;
+  p.out_row = c.out_row;
+  p.m = c.a->rows;
+  p.n = c.w->rows;
+  p.group_tiles = mx_group_tiles(FMT, c.a->cols);
+  p.row_bytes_used = (int)(c.a->cols * mx_bits(FMT) / 8);
+  p.err = c.err;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.n + 127) / 128), (unsigned)((p.m + TN - 1) / TN), 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = c.stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = c.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
+}
+
+template <int FMT>
+cudaError_t launch_format(const ProductCall& c) {
+  if (c.a->rows <= 16) return launch<FMT, 16>(c);
+  if (c.a->rows <= 32) return launch<FMT, 32>(c);
+  if (c.a->rows <= 64) return launch<FMT, 64>(c);
+  return launch<FMT, 128>(c);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_product(const ProductCall& c) {
+  switch (c.a->format) {
+    case ATTN_RES_MXFP8: return launch_format<ATTN_RES_MXFP8>(c);
+    case ATTN_RES_MXFP4: return launch_format<ATTN_RES_MXFP4>(c);
+    case ATTN_RES_NVFP4: return launch_format<ATTN_RES_NVFP4>(c);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn_res_host

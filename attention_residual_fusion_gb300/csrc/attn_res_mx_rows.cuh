@@ -1,0 +1,231 @@
+// attn_res_mx_rows.cuh -- rows to and from the microscaled formats:
+// quantisation, its inverse, and the residual addition + RMSNorm whose result
+// is quantised.  All three are bound by memory: a group's scale needs only
+// its 16 or 32 elements (two or four lanes of eight), so a row is read once
+// and its codes and scales are written from the registers it was read into.
+#pragma once
+
+#include "attn_res_mx.cuh"
+
+namespace attn_res_dev {
+
+// ---- quantisation -------------------------------------------------------------------
+//
+// A warp takes 256 columns of the four rows r, r + 32, r + 64, r + 96 of a
+// 128-row tile: those rows' scales of four groups are the 16 consecutive
+// bytes of one entry of a scale tile, so a lane stores them at once, and the
+// entries of rows and groups that do not exist come out as zeros by the same
+// stores.  Four 16-byte loads per lane are in flight.
+constexpr int kMxThreads = 256;
+constexpr int kMxWarpCols = 256;
+
+struct MxRowsParams {
+  const uint16_t* x;  // quantise: source
+  uint16_t* out;      // dequantise: result
+  int64_t x_row;
+  MxView q;
+  int64_t col_chunks;  // ceil(padded cols / 256)
+  int64_t jobs;        // row tiles * 32 * col_chunks
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kMxThreads) attn_res_mx_quantize_kernel(const MxRowsParams p) {
+  using M = Mx<FMT>;
+  const int lane = threadIdx.x & 31;
+  const int64_t job = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
+  const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
+  const float g6 = 6.f * g;
+  grid_dep_wait();
+  if (job < p.jobs) {
+    const int64_t chunk = job % p.col_chunks;
+    const int64_t rest = job / p.col_chunks;
+    const int r = (int)(rest & 31);
+    const int64_t tile = rest >> 5;
+    const int64_t vec = chunk * 32 + lane;
+    const bool in_row = vec * 8 < p.q.cols;
+    uint4 v[4];
+    bool ok[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t row = tile * 128 + 32 * u + r;
+      ok[u] = in_row && row < p.q.rows;
+      v[u] = ok[u] ? ld_row(p.x + row * p.x_row + vec * 8) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t word[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[8];
+      widen8(v[u], x);
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) am = max(am, abs_bits(x[i]));
+      const GroupScale<FMT> s = group_scale<FMT>(group_max<M::LANES>(am), g, g6);
+      if (ok[u])
+        st_codes<FMT>(p.q.data + (tile * 128 + 32 * u + r) * p.q.row_bytes, vec, encode8<FMT>(x, s.by));
+      word[u] = scale_word<FMT>(ok[u] ? s.code : 0u);
+    }
+    const int64_t atom = vec / M::ATOM_LANES;
+    if (lane % M::ATOM_LANES == 0 && atom < p.q.group_tiles)
+      *reinterpret_cast<uint4*>(p.q.scales + ((tile * p.q.group_tiles + atom) * 512 + r * 16)) =
+          make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  grid_dep_launch_dependents();
+}
+
+// ---- the inverse ---------------------------------------------------------------------
+
+template <int FMT>
+__global__ void __launch_bounds__(kMxThreads) attn_res_mx_dequantize_kernel(const MxRowsParams p) {
+  using M = Mx<FMT>;
+  const int lane = threadIdx.x & 31;
+  const int64_t job = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
+  const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
+  grid_dep_wait();
+  if (job < p.jobs) {
+    const int64_t chunk = job % p.col_chunks;
+    const int64_t rest = job / p.col_chunks;
+    const int r = (int)(rest & 31);
+    const int64_t tile = rest >> 5;
+    const int64_t vec = chunk * 32 + lane;
+    if (vec * 8 < p.q.cols) {
+      const int64_t group = vec / M::LANES;
+      const uint4 sc = *reinterpret_cast<const uint4*>(
+          p.q.scales + ((tile * p.q.group_tiles + group / 4) * 512 + r * 16));
+      Codes<FMT> c[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t row = tile * 128 + 32 * u + r;
+        if (row < p.q.rows) c[u] = ld_codes<FMT>(p.q.data + row * p.q.row_bytes, vec);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t row = tile * 128 + 32 * u + r;
+        if (row >= p.q.rows) break;
+        const uint32_t code = (vword(sc, u) >> (8 * (int)(group % 4))) & 0xffu;
+        const float s = M::NV ? e4m3_value(code) : e8m0_value(code);
+        float x[8];
+        decode8<FMT>(c[u], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = M::NV ? x[i] * s * g : x[i] * s;
+        st_row(p.out + row * p.x_row + vec * 8,
+               make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+      }
+    }
+  }
+  grid_dep_launch_dependents();
+}
+
+// ---- residual addition + RMSNorm + quantisation ---------------------------------------
+//
+// One CTA per token row, the row in registers (VPT 16-byte vectors per
+// thread); the sum of c^2 takes one CTA barrier.  CTAs behind the last row
+// write the zero scale entries of the rows that pad the last 128-row tile,
+// kPadRows of them each.
+constexpr int kMxNormMaxThreads = 1024;
+constexpr int kMxPadRows = 8;
+
+struct MxNormParams {
+  uint16_t* prefix;
+  const uint16_t* delta;
+  const uint16_t* weight;
+  uint16_t* norm_out;
+  int64_t prefix_row, delta_row, norm_row;
+  float eps, inv_h;
+  MxView q;
+};
+
+template <int FMT, int VPT>
+__global__ void __launch_bounds__(VPT == 8 ? kMxNormMaxThreads : 256)
+    attn_res_mx_norm_kernel(const MxNormParams p) {
+  using M = Mx<FMT>;
+  __shared__ float part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t = blockIdx.x;
+  const int nv = (int)(p.q.cols / 8);
+  if (t >= p.q.rows) {
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    const int64_t first = p.q.rows + (t - p.q.rows) * kMxPadRows;
+    const int64_t last = (p.q.rows + 127) / 128 * 128;
+    for (int64_t row = first; row < first + kMxPadRows && row < last; ++row)
+      for (int64_t a = tid; a < p.q.group_tiles; a += blockDim.x)
+        *reinterpret_cast<uint32_t*>(p.q.scales + ((row / 128) * p.q.group_tiles + a) * 512 +
+                                     (row % 32) * 16 + (row % 128) / 32 * 4) = 0u;
+    return;
+  }
+  uint4 w[VPT], c[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int i = tid + v * blockDim.x;
+    w[v] = i < nv ? ld_weight(p.weight + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
+  }
+  const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
+  const float g6 = 6.f * g;
+  grid_dep_wait();
+  uint16_t* const prow = p.prefix + t * p.prefix_row;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int i = tid + v * blockDim.x;
+    c[v] = i < nv ? ld_row(prow + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
+  }
+  if (p.delta) {
+    uint4 d[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int i = tid + v * blockDim.x;
+      d[v] = i < nv ? ld_row(p.delta + t * p.delta_row + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) c[v] = add_bf16x8(c[v], d[v]);
+  }
+  grid_dep_launch_dependents();
+  float sq = 0.f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    float x[8];
+    widen8(c[v], x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+  }
+  sq = warp_sum(sq);
+  if (lane == 0) part[warp] = sq;
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  const float tot = warp_sum(lane < warps ? part[lane] : 0.f);
+  const float rstd = __frsqrt_rn(fmaf(tot, p.inv_h, p.eps));
+  uint8_t* const qrow = p.q.data + t * p.q.row_bytes;
+  uint8_t* const srow =
+      p.q.scales + (t / 128) * p.q.group_tiles * 512 + (t % 32) * 16 + (t % 128) / 32 * 4;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int i = tid + v * blockDim.x;
+    const bool in_row = i < nv;
+    float x[8], wf[8];
+    widen8(c[v], x);
+    widen8(w[v], wf);
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // c * w is exact in fp32 (two 8-bit significands), so y is rounded once;
+      // past the row's end the zeros stay zeros, whatever the row's statistics
+      x[k] = in_row ? x[k] * wf[k] * rstd : 0.f;
+      am = max(am, abs_bits(x[k]));
+    }
+    const GroupScale<FMT> s = group_scale<FMT>(group_max<M::LANES>(am), g, g6);
+    if (in_row) {
+      st_codes<FMT>(qrow, i, encode8<FMT>(x, s.by));
+      if (p.norm_out)
+        st_row(p.norm_out + t * p.norm_row + (int64_t)i * 8,
+               make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+      if (p.delta) st_row(prow + (int64_t)i * 8, c[v]);
+    }
+    const uint32_t word = scale_word<FMT>(in_row ? s.code : 0u);
+    const int atom = i / M::ATOM_LANES;
+    if (lane % M::ATOM_LANES == 0 && atom < p.q.group_tiles)
+      *reinterpret_cast<uint32_t*>(srow + (int64_t)atom * 512) = word;
+  }
+}
+
+}  // namespace attn_res_dev

@@ -325,6 +325,113 @@ attn_res_status_t attn_res_tp_finish(int64_t Hs, int64_t H, attn_res_bf16_t* pre
                                      attn_res_bf16_t* out, int64_t T,
                                      const attn_res_layout_t* layout, void* stream);
 
+/*
+ * Microscaled rows: a row is held as 8- or 4-bit elements with a scale for
+ * each group of 16 or 32 neighbours (the OCP Microscaling Formats
+ * specification's MXFP8 and MXFP4, and the NVFP4 variant), the form in which
+ * a projection after the mixture takes its input.  The calls below bring
+ * rows into it (after a residual addition and RMSNorm, or as they are), back
+ * to bf16, and multiply two such matrices.  (No counterpart on the pages,
+ * whose mixture ends with a bf16 row.)
+ *
+ *   format            element  group  scale of a group         scale of the tensor
+ *   ATTN_RES_MXFP8    e4m3     32     e8m0 (a power of two)    none
+ *   ATTN_RES_MXFP4    e2m1     32     e8m0                     none
+ *   ATTN_RES_NVFP4    e2m1     16     e4m3                     fp32, optional
+ *
+ * An element x of a group with scale s in a tensor with scale g (1 without
+ * one) stands for code * s * g.  Quantisation, with TOP = 448 (e4m3) or 6
+ * (e2m1), amax the group's largest |x|, rn = round to nearest, ties to even:
+ *   MXFP8, MXFP4: s = the smallest power of two >= 2^-127 with
+ *                 amax <= TOP * s (so nothing is clipped); code = rn(x / s);
+ *   NVFP4:        s = rn_e4m3(min(448, amax / (6 g))), code = rn(x / (s g)),
+ *                 0 where s g == 0, clipped to +-6 (fp32 operations, each
+ *                 correctly rounded: 6 g, the two quotients and s g).
+ * A group that holds a NaN or an infinity gets the scale NaN and zero
+ * elements: it stands for NaN throughout.  g must be finite and > 0.
+ *
+ * Data: element k of row r is the byte data[r * row_bytes + k] (8 bits), or
+ * the low (even k) or high (odd k) half of data[r * row_bytes + k / 2] (4
+ * bits).  cols must be a multiple of 32, data 16-byte aligned and row_bytes
+ * a multiple of 16; bytes past the row's last are neither read nor written.
+ * Scales: tiles of 128 rows x 4 groups, 512 bytes each, row tiles outermost
+ * and without gaps: the scale of row r and group j is byte
+ *   ((r / 128) * ceil(groups / 4) + j / 4) * 512
+ *     + (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4,
+ * the order in which the tensor cores take them.  The buffer holds
+ * attn_res_mx_scale_bytes(format, rows, cols) bytes, 16-byte aligned; the
+ * entries past the last row and the last group are written as 0, and
+ * attn_res_mx_matmul wants those past the last group to be 0.
+ */
+#define ATTN_RES_MXFP8 1
+#define ATTN_RES_MXFP4 2
+#define ATTN_RES_NVFP4 3
+
+typedef struct {
+  int32_t format;            /* ATTN_RES_MXFP8, ATTN_RES_MXFP4 or ATTN_RES_NVFP4 */
+  int64_t rows, cols;        /* rows >= 0; cols > 0, a multiple of 32 */
+  void* data;                /* element codes */
+  int64_t row_bytes;         /* between rows of data */
+  uint8_t* scales;           /* tiled scales */
+  const float* tensor_scale; /* g: one fp32 on the device (4-byte aligned), or NULL;
+                                NULL unless format is ATTN_RES_NVFP4 */
+} attn_res_mx_t;
+
+/* Bytes of the scale buffer; -1 for an unknown format, rows < 0, or cols not
+ * a positive multiple of 32 (or too large for the product to fit). */
+int64_t attn_res_mx_scale_bytes(int format, int64_t rows, int64_t cols);
+
+/*
+ * The calls below take device pointers of the current device and enqueue on
+ * `stream` as attn_res does; flags is 0 or ATTN_RES_FLAG_PDL (weight and
+ * tensor-scale arguments, and attn_res_mx_matmul's w, may then be read before
+ * the preceding kernel has finished; everything else is read, and everything
+ * is written, after it).  bf16 rows have unit inner stride, 16-byte aligned
+ * pointers and row strides that are multiples of 8 elements and >= the row
+ * width.  A written range that overlaps another argument's is
+ * ATTN_RES_EALIAS; the other errors are as for attn_res, before any launch.
+ * With no rows (for the product: no rows in a or in w) a call checks the
+ * scalar arguments and returns OK.
+ */
+
+/* q = x [q->rows, q->cols] in q's format; writes q's data and scales. */
+attn_res_status_t attn_res_mx_quantize(const attn_res_bf16_t* x, int64_t x_row,
+                                       const attn_res_mx_t* q, uint32_t flags, void* stream);
+
+/* x = the bf16 values that q stands for (element * s, then * g, in fp32,
+ * rounded to bf16 once). */
+attn_res_status_t attn_res_mx_dequantize(const attn_res_mx_t* q, attn_res_bf16_t* x,
+                                         int64_t x_row, uint32_t flags, void* stream);
+
+/*
+ * attn_res_mx_norm -- residual addition, RMSNorm and quantisation of q->rows
+ * token rows of width H = q->cols (at most 65536):
+ *
+ *   c = bf16_rn(prefix[t] + delta[t])   (c = prefix[t] if delta == NULL)
+ *   y = c * weight / sqrt(mean(c^2) + eps)
+ *   prefix[t] = c                       when delta != NULL (in place)
+ *   norm_out[t] = bf16_rn(y)            when norm_out != NULL
+ *   q[t] = y in q's format              (from the fp32 y)
+ *
+ * the mixture's current row and output norm (as attn_res with no bank rows),
+ * its result in the microscaled form.  eps is finite and >= 0.
+ */
+attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
+                                   const attn_res_bf16_t* delta, int64_t delta_row,
+                                   const attn_res_bf16_t* weight, float eps,
+                                   attn_res_bf16_t* norm_out, int64_t norm_row,
+                                   const attn_res_mx_t* q, uint32_t flags, void* stream);
+
+/*
+ * attn_res_mx_matmul -- out[m, n] = sum_k a[m, k] w[n, k], out
+ * [a->rows, w->rows] bf16 at out_row, for two matrices of one format and
+ * width (a->cols == w->cols); fp32 sums on the tensor cores (tcgen05, block
+ * scaled), rounded to bf16 once.  Any number of rows on both sides.
+ */
+attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t* w,
+                                     attn_res_bf16_t* out, int64_t out_row, uint32_t flags,
+                                     void* stream);
+
 /* Static text for a status code. */
 const char* attn_res_status_string(attn_res_status_t status);
 
