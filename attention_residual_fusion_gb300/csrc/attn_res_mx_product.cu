@@ -42,21 +42,41 @@ cudaError_t operand_map(const attn_res_mx_t& x, uint32_t rows, CUtensorMap* map)
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int FMT, int TN>
-cudaError_t launch(const ProductCall& c) {
-  using C = ProductCfg<FMT, TN>;
-  void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_kernel<FMT, TN>;
-  static std::atomic<uint64_t> enabled{0};
-  const uint64_t bit = 1ull << c.device;
-  if (!(enabled.load(std::memory_order_acquire) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-    if (e != cudaSuccess) return e;
-    enabled.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  CUtensorMap map_a, map_w;
-  cudaError_t e = operand_map(*c.a, TN, &map_a);
-  if (e == cudaSuccess) e = operand_map(*c.w, 128, &map_w);
+// Of its scales: rows of 512 bytes (one tile of 128 rows x 4 groups), boxes of
+// the tiles of one 128-byte block of codes.
+cudaError_t scales_map(const attn_res_mx_t& x, uint32_t tiles, CUtensorMap* map) {
+  EncodeTiled enc;
+  cudaError_t e = encode_tiled(&enc);
   if (e != cudaSuccess) return e;
+  const cuuint64_t dim[2] = {128, (cuuint64_t)((x.rows + 127) / 128 * mx_group_tiles(x.format, x.cols))};
+  const cuuint64_t stride[1] = {512};
+  const cuuint32_t box[2] = {128, tiles};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, x.scales, dim, stride, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Of the result's columns up to the last 16-byte boundary: boxes of 64 columns
+// x 32 rows, 128-byte swizzle (at least one boundary, which then no store uses).
+cudaError_t out_map(const ProductCall& c, CUtensorMap* map) {
+  EncodeTiled enc;
+  cudaError_t e = encode_tiled(&enc);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t whole = (cuuint64_t)(c.w->rows / 8 * 8);
+  const cuuint64_t dim[2] = {whole ? whole : 8, (cuuint64_t)c.a->rows};
+  const cuuint64_t stride[1] = {(cuuint64_t)c.out_row * 2};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t one[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.out, dim, stride, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int FMT>
+ProductParams params(const ProductCall& c) {
   ProductParams p = {};
   p.a_scales = c.a->scales;
   p.w_scales = c.w->scales;
@@ -69,6 +89,32 @@ cudaError_t launch(const ProductCall& c) {
   p.group_tiles = mx_group_tiles(FMT, c.a->cols);
   p.row_bytes_used = (int)(c.a->cols * mx_bits(FMT) / 8);
   p.err = c.err;
+  return p;
+}
+
+// The dynamic shared memory above 48 KB is opt-in, per function and device.
+template <class Kern>
+cudaError_t allow_smem(Kern kern, uint32_t bytes, int device, std::atomic<uint64_t>& enabled) {
+  const uint64_t bit = 1ull << device;
+  if (!(enabled.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    enabled.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  return cudaSuccess;
+}
+
+template <int FMT, int TN>
+cudaError_t launch(const ProductCall& c) {
+  using C = ProductCfg<FMT, TN>;
+  void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_kernel<FMT, TN>;
+  static std::atomic<uint64_t> enabled{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
+  CUtensorMap map_a, map_w;
+  if (e == cudaSuccess) e = operand_map(*c.a, TN, &map_a);
+  if (e == cudaSuccess) e = operand_map(*c.w, 128, &map_w);
+  if (e != cudaSuccess) return e;
+  const ProductParams p = params<FMT>(c);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -83,11 +129,54 @@ cudaError_t launch(const ProductCall& c) {
 }
 
 template <int FMT>
+cudaError_t launch_wide(const ProductCall& c) {
+  using C = WideCfg<FMT>;
+  void (*kern)(ProductParams, TileWalk, WideMaps) = attn_res_mx_product_wide_kernel<FMT>;
+  static std::atomic<uint64_t> enabled{0};
+  static std::atomic<int> pairs_of[64];
+  cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
+  WideMaps maps;
+  if (e == cudaSuccess) e = operand_map(*c.a, 128, &maps.a);
+  if (e == cudaSuccess) e = operand_map(*c.w, 128, &maps.w);
+  if (e == cudaSuccess) e = scales_map(*c.a, C::F::ATOMS, &maps.a_sf);
+  if (e == cudaSuccess) e = scales_map(*c.w, C::F::ATOMS, &maps.w_sf);
+  if (e == cudaSuccess) e = out_map(c, &maps.out);
+  if (e != cudaSuccess) return e;
+  const ProductParams p = params<FMT>(c);
+  const TileWalk walk{(p.m + C::TM - 1) / C::TM, (p.n + C::TN - 1) / C::TN};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = pairs_of[c.device].load(std::memory_order_acquire);
+  if (pairs == 0) {  // pairs that the device holds at once
+    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    pairs_of[c.device].store(pairs, std::memory_order_release);
+  }
+  const int64_t tiles = walk.m_tiles * walk.n_tiles;
+  cfg.gridDim.x = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
+  cfg.numAttrs = c.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, walk, maps);
+}
+
+template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
   if (c.a->rows <= 16) return launch<FMT, 16>(c);
   if (c.a->rows <= 32) return launch<FMT, 32>(c);
   if (c.a->rows <= 64) return launch<FMT, 64>(c);
-  return launch<FMT, 128>(c);
+  if (c.a->rows <= 128) return launch<FMT, 128>(c);
+  return launch_wide<FMT>(c);
 }
 
 }  // namespace
