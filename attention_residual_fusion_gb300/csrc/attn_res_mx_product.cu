@@ -1,4 +1,6 @@
 // attn_res_mx_product.cu -- launches of the microscaled product.
+#include <cstdio>
+#include <cstdlib>
 #include "attn_res_mx_host.cuh"
 
 namespace attn_res_host {
@@ -104,10 +106,29 @@ cudaError_t allow_smem(Kern kern, uint32_t bytes, int device, std::atomic<uint64
   return cudaSuccess;
 }
 
+struct Attributes {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  Attributes(dim3 grid, int threads, uint32_t smem, unsigned cluster, const ProductCall& c) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.pdl ? 2 : 1;
+  }
+  Attributes(const Attributes&) = delete;
+};
+
 template <int FMT, int TN>
-cudaError_t launch(const ProductCall& c) {
-  using C = ProductCfg<FMT, TN>;
-  void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_kernel<FMT, TN>;
+cudaError_t launch_narrow(const ProductCall& c) {
+  using C = NarrowCfg<FMT, TN>;
+  void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_narrow_kernel<FMT, TN>;
   static std::atomic<uint64_t> enabled{0};
   cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
   CUtensorMap map_a, map_w;
@@ -115,17 +136,15 @@ cudaError_t launch(const ProductCall& c) {
   if (e == cudaSuccess) e = operand_map(*c.w, 128, &map_w);
   if (e != cudaSuccess) return e;
   const ProductParams p = params<FMT>(c);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.n + 127) / 128), (unsigned)((p.m + TN - 1) / TN), 1);
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = c.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = c.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p, map_a, map_w);
+  const int64_t n_tiles = (p.n + 127) / 128, m_tiles = (p.m + TN - 1) / TN;
+  const int blocks = (p.row_bytes_used + 127) / 128;
+  static const int want = getenv("SPLIT") ? atoi(getenv("SPLIT")) : 0;
+  int64_t split = 304 / (n_tiles * m_tiles);
+  split = split > 8 ? 8 : split < 1 ? 1 : split;
+  if (want) split = want;
+  if (split > blocks) split = blocks;
+  Attributes l(dim3((unsigned)(n_tiles * split), (unsigned)m_tiles, 1), C::THREADS, C::SMEM, (unsigned)split, c);
+  return cudaLaunchKernelEx(&l.cfg, kern, p, map_a, map_w);
 }
 
 template <int FMT>
@@ -143,39 +162,29 @@ cudaError_t launch_wide(const ProductCall& c) {
   if (e == cudaSuccess) e = out_map(c, &maps.out);
   if (e != cudaSuccess) return e;
   const ProductParams p = params<FMT>(c);
-  const TileWalk walk{(p.m + C::TM - 1) / C::TM, (p.n + C::TN - 1) / C::TN};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const int64_t m_tiles = (p.m + C::TM - 1) / C::TM, n_tiles = (p.n + C::TN - 1) / C::TN;
+  const int64_t tiles = m_tiles * n_tiles;
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const TileWalk walk{(int)m_tiles, (int)n_tiles};
+  Attributes l(dim3(2, 1, 1), C::THREADS, C::SMEM, 2, c);
   int pairs = pairs_of[c.device].load(std::memory_order_acquire);
-  if (pairs == 0) {  // pairs that the device holds at once
-    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg);
+  if (pairs == 0) {  // that the device holds at once
+    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &l.cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     pairs_of[c.device].store(pairs, std::memory_order_release);
   }
-  const int64_t tiles = walk.m_tiles * walk.n_tiles;
-  cfg.gridDim.x = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-  cfg.numAttrs = c.pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, walk, maps);
+  l.cfg.gridDim.x = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
+  return cudaLaunchKernelEx(&l.cfg, kern, p, walk, maps);
 }
 
 template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
-  if (c.a->rows <= 16) return launch<FMT, 16>(c);
-  if (c.a->rows <= 32) return launch<FMT, 32>(c);
-  if (c.a->rows <= 64) return launch<FMT, 64>(c);
-  if (c.a->rows <= 128) return launch<FMT, 128>(c);
+  static const int wide = getenv("WIDE") ? atoi(getenv("WIDE")) : 256;
+  if (c.a->rows <= 16) return launch_narrow<FMT, 16>(c);
+  if (c.a->rows <= 32) return launch_narrow<FMT, 32>(c);
+  if (c.a->rows <= 64) return launch_narrow<FMT, 64>(c);
+  if (c.a->rows <= wide) return launch_narrow<FMT, 128>(c);
   return launch_wide<FMT>(c);
 }
 

@@ -35,26 +35,45 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// An arrival that orders nothing in shared or global memory: it tells that
+// this thread's TMEM loads are complete (they are: tcgen05.wait::ld has
+// returned, and tcgen05.fence::before_thread_sync keeps them before it).  With
+// release semantics it waited about 2000 clocks for the warp's earlier stores.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// mbar_wait_bounded and wait_or_flag for a barrier that other CTAs arrive on.
-__device__ __forceinline__ void wait_or_flag_cluster(uint32_t bar, uint32_t parity, bool& failed,
-                                                     unsigned* err, unsigned bit) {
-  if (failed) return;
-  const uint64_t t0 = global_timer_ns();
+// The bounded waits of these kernels: as wait_or_flag, with the clock (whose
+// reading takes longer than a stage's wait) looked at only from the 256th try
+// on.  PEERS: the barrier is arrived on by other CTAs of the cluster too.
+template <bool PEERS = false>
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity) {
+  if constexpr (!PEERS) return mbar_try_wait(bar, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <bool PEERS = false>
+__device__ __forceinline__ bool phase_wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return;
-    if ((it & 1023u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) break;
+    if (phase_done<PEERS>(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
   }
+}
+template <bool PEERS = false>
+__device__ __forceinline__ void phase_or_flag(uint32_t bar, uint32_t parity, bool& failed, unsigned* err,
+                                              unsigned bit) {
+  if (failed || phase_wait<PEERS>(bar, parity)) return;
   failed = true;
   atomicOr(err, bit);
 }
@@ -112,14 +131,32 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t tmem, uint64_t desc) {
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads that gave r are complete (r passes through, so that nothing uses
+// it before).
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr));
+}
+// The loads that gave r are complete (r passes through, so that nothing uses
+// it before).
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+               :
+               : "memory");
+}
 
 #define ATTN_RES_MMA_SCALED(GROUP, KIND)                                                         \
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                                 \
@@ -143,16 +180,28 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 }
 #undef ATTN_RES_MMA_SCALED
 
-// Shared-memory descriptor of a K-major operand in 128-byte swizzled rows
-// (eight rows of 128 bytes = 1024 bytes between row groups).
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory descriptors: the low word is the address in 16-byte units (and
+// a leading offset that these layouts do not use), the high word a constant
+// of the layout, so that steps within a stage are small additions.
+// Operands: K-major rows of 128 swizzled bytes, eight rows (1024 bytes) apart.
+constexpr uint32_t kOperandHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+// Scales: 32 rows of 16 bytes, not swizzled, eight rows (128 bytes) apart.
+constexpr uint32_t kScalesHi = (128u >> 4) | 1u << 14;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | 1u << 16; }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
 }
-// Of a 32 x 16-byte scale tile, not swizzled (128 bytes between groups of
-// eight rows).
-__device__ __forceinline__ uint64_t scales_desc(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // A 128-byte block of a K-major row: 128 e4m3 elements or 256 e2m1, taken by
@@ -176,6 +225,48 @@ __device__ __forceinline__ uint32_t step_idesc(uint32_t idesc, int j) {
   return idesc | id << 4 | id << 29;
 }
 
+// What the tensor cores do with one 128-byte block of K: scales to TMEM, then
+// `STEPS` products of 32 bytes.  P is the operand on the M side (128 rows a
+// CTA), Q the one on the N side, whose scales come in QT tiles of 128 rows.
+// Issued by one thread; all addresses are its first CTA's.
+template <int FMT, int G, int QT, int STEPS>
+__device__ __forceinline__ void block_products(uint32_t acc, uint32_t sf, uint32_t p_lo, uint32_t q_lo,
+                                               uint32_t psf_lo, uint32_t qsf_lo, uint32_t idesc,
+                                               uint32_t accumulate) {
+  using F = ProductFmt<FMT>;
+  constexpr int ATOMS = (STEPS + F::STEPS_PER_ATOM - 1) / F::STEPS_PER_ATOM;
+  constexpr uint32_t TILE = 512 >> 4;  // a scale tile, in descriptor units
+#pragma unroll
+  for (int t = 0; t < ATOMS; ++t) {
+    scales_to_tmem<G>(sf + 4 * t, desc_of(psf_lo + TILE * t, kScalesHi));
+#pragma unroll
+    for (int h = 0; h < QT; ++h)  // the row tiles of one group tile side by side
+      scales_to_tmem<G>(sf + F::ATOMS * 4 + 4 * (QT * t + h),
+                        desc_of(qsf_lo + TILE * (F::ATOMS * h + t), kScalesHi));
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int t = j / F::STEPS_PER_ATOM;
+    mma_scaled<FMT, G>(acc, desc_of(p_lo + 2 * j, kOperandHi), desc_of(q_lo + 2 * j, kOperandHi),
+                       step_idesc<FMT>(idesc, j), sf + 4 * t, sf + F::ATOMS * 4 + 4 * QT * t,
+                       j > 0 ? 1u : accumulate);
+  }
+}
+// The same for a block of `bytes` <= 128 bytes.
+template <int FMT, int G, int QT>
+__device__ __forceinline__ void block_products_of(int bytes, uint32_t acc, uint32_t sf, uint32_t p_lo,
+                                                  uint32_t q_lo, uint32_t psf_lo, uint32_t qsf_lo,
+                                                  uint32_t idesc, uint32_t accumulate) {
+  if (bytes > 96)
+    block_products<FMT, G, QT, 4>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
+  else if (bytes > 64)
+    block_products<FMT, G, QT, 3>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
+  else if (bytes > 32)
+    block_products<FMT, G, QT, 2>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
+  else
+    block_products<FMT, G, QT, 1>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
+}
+
 struct ProductParams {
   const uint8_t* a_scales;
   const uint8_t* w_scales;
@@ -189,46 +280,51 @@ struct ProductParams {
   unsigned* err;
 };
 
-// ---- weight rows on the instruction's M side ----------------------------------------------
+// ---- few tokens: weight rows on the instruction's M side, K split over a cluster -----------
 //
-// A CTA makes 128 output columns (weight rows, the instruction's M) for TN
-// tokens (its N).  TN < 128 only with a single token tile: a tile's token
+// A CTA makes a part of the sums of 128 output columns (weight rows, the
+// instruction's M) for TN tokens (its N): the part of its range of K.  The
+// CTAs of a cluster share one tile and split K evenly; their parts meet in
+// shared memory and are added up in rank order.  TN < 128 only with a single token tile: a tile's token
 // scales then start at the first of their scale tile's columns.
+constexpr int kMaxSplit = 8;  // the portable cluster size
+
 template <int FMT, int TN>
-struct ProductCfg {
+struct NarrowCfg {
   using F = ProductFmt<FMT>;
   static constexpr uint32_t W_BYTES = 128 * 128;
   static constexpr uint32_t A_BYTES = TN * 128;
   static constexpr uint32_t SF_BYTES = F::ATOMS * 512;
   static constexpr uint32_t STAGE = W_BYTES + A_BYTES + 2 * SF_BYTES;
-  static constexpr int STAGES = 4;
-  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
+  // two CTAs an SM, each with as many stages as half of its shared memory
+  // (227 KB less 1 KB a CTA) and half of TMEM hold
+  static constexpr int STAGES = (112 * 1024 - 1024) / STAGE;
   // TMEM columns: the accumulator, then for each stage its scales (so that a
   // stage's scales are replaced only after the products that read them)
   static constexpr int SF_COLS = F::ATOMS * 4;
   static constexpr int COLS_USED = TN + STAGES * 2 * SF_COLS;
   static constexpr int COLS = pow2_at_least(COLS_USED < 32 ? 32 : COLS_USED);
-  static_assert(COLS <= 512, "TMEM");
+  static_assert(STAGES >= 2 && COLS <= 256, "two CTAs an SM");
+  static constexpr uint32_t PARTS = TN * 128 * 4;  // fp32 sums of the tile, over the stages
+  static constexpr uint32_t SMEM = (STAGES * STAGE > PARTS ? STAGES * STAGE : PARTS) + 1024;
   static constexpr int THREADS = 192;
 };
 
 template <int FMT, int TN>
 __global__ void __launch_bounds__(192)
-    attn_res_mx_product_kernel(const ProductParams p, const __grid_constant__ CUtensorMap map_a,
-                               const __grid_constant__ CUtensorMap map_w) {
-  using C = ProductCfg<FMT, TN>;
+    attn_res_mx_product_narrow_kernel(const ProductParams p, const __grid_constant__ CUtensorMap map_a,
+                                      const __grid_constant__ CUtensorMap map_w) {
+  using C = NarrowCfg<FMT, TN>;
   using F = ProductFmt<FMT>;
   constexpr int S = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long bars[2 * S + 1];
   __shared__ uint32_t tmem_slot;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), split = (int)cluster_nctarank();
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * S, done = empty + 8 * S;
-  auto w_at = [&](int s) { return base + s * C::W_BYTES; };
-  auto a_at = [&](int s) { return base + S * C::W_BYTES + s * C::A_BYTES; };
-  auto wsf_at = [&](int s) { return base + S * (C::W_BYTES + C::A_BYTES) + s * 2 * C::SF_BYTES; };
-  auto asf_at = [&](int s) { return wsf_at(s) + C::SF_BYTES; };
+  const uint32_t w_at = base, a_at = base + S * C::W_BYTES, sf_at = base + S * (C::W_BYTES + C::A_BYTES);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
     fence_mbar_init();
@@ -237,82 +333,148 @@ __global__ void __launch_bounds__(192)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const int64_t n0 = (int64_t)blockIdx.x * 128, m0 = (int64_t)blockIdx.y * TN;
-  const int blocks = (p.row_bytes_used + 127) / 128;
-  grid_dep_wait();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
+  const int n0 = (int)(blockIdx.x / split) * 128, m0 = (int)blockIdx.y * TN;
+  const int all_blocks = (p.row_bytes_used + 127) / 128;
+  const int kb0 = (int)((int64_t)all_blocks * rank / split);
+  const int blocks = (int)((int64_t)all_blocks * (rank + 1) / split) - kb0;
+  bool failed = false;
+  // the output may still be in use by the preceding kernel; the loading thread
+  // waits later
+  if (threadIdx.x != 0) grid_dep_wait();
 
   if (warp == 0 && lane == 0) {
-    bool failed = false;
-    const uint8_t* wsf = p.w_scales + (n0 / 128) * p.group_tiles * 512;
-    const uint8_t* asf = p.a_scales + (m0 / 128) * p.group_tiles * 512;
-    int issued = 0;
-    for (int kb = 0; kb < blocks; ++kb) {
-      const int s = kb % S, use = kb / S;
-      if (use > 0) wait_or_flag(empty + 8 * s, (use - 1) & 1, failed, p.err, kErrStageTimeout);
-      if (failed) break;
+    const uint8_t* wsf = p.w_scales + (int64_t)(n0 / 128) * p.group_tiles * 512;
+    const uint8_t* asf = p.a_scales + (int64_t)(m0 / 128) * p.group_tiles * 512;
+    // the weights do not depend on the preceding kernel: the first stages'
+    // are on their way before the wait for it
+    const int ahead = blocks < S ? blocks : S;
+    auto sf_bytes = [&](int kb) {
       const int64_t left = p.group_tiles - (int64_t)kb * F::ATOMS;
-      const uint32_t sf = (uint32_t)(left < F::ATOMS ? left : F::ATOMS) * 512u;
-      const uint32_t bar = full + 8 * s;
+      return (uint32_t)(left < F::ATOMS ? left : F::ATOMS) * 512u;
+    };
+    auto load_w = [&](int i, int s) {
+      const int kb = kb0 + i;
+      const uint32_t bar = full + 8 * s, sf = sf_bytes(kb);
       mbar_arrive_expect_tx(bar, C::W_BYTES + C::A_BYTES + 2 * sf);
-      tma_load_2d(w_at(s), &map_w, kb * 128, (int)n0, bar);
-      tma_load_2d(a_at(s), &map_a, kb * 128, (int)m0, bar);
-      bulk_load(wsf_at(s), wsf + (int64_t)kb * F::ATOMS * 512, sf, bar);
-      bulk_load(asf_at(s), asf + (int64_t)kb * F::ATOMS * 512, sf, bar);
-      issued = kb + 1;
+      tma_load_2d(w_at + s * C::W_BYTES, &map_w, kb * 128, n0, bar);
+      bulk_load(sf_at + s * 2 * C::SF_BYTES, wsf + (int64_t)kb * F::ATOMS * 512, sf, bar);
+    };
+    auto load_a = [&](int i, int s) {
+      const int kb = kb0 + i;
+      const uint32_t bar = full + 8 * s;
+      tma_load_2d(a_at + s * C::A_BYTES, &map_a, kb * 128, m0, bar);
+      bulk_load(sf_at + s * 2 * C::SF_BYTES + C::SF_BYTES, asf + (int64_t)kb * F::ATOMS * 512, sf_bytes(kb), bar);
+    };
+    for (int i = 0; i < ahead; ++i) load_w(i, i);
+    grid_dep_wait();
+    for (int i = 0; i < ahead; ++i) load_a(i, i);
+    int issued = ahead;
+    for (int i = ahead; i < blocks; ++i) {
+      const int s = i % S;
+      phase_or_flag(empty + 8 * s, (i / S - 1) & 1, failed, p.err, kErrStageTimeout);
+      if (failed) break;
+      load_w(i, s);
+      load_a(i, s);
+      issued = i + 1;
     }
     if (failed)  // copies still in flight land before the CTA ends
-      for (int kb = issued > S ? issued - S : 0; kb < issued; ++kb)
-        (void)mbar_wait_bounded(full + 8 * (kb % S), (kb / S) & 1);
-  } else if (warp == 1 && lane == 0) {
-    bool failed = false;
-    const uint32_t idesc = F::idesc(128, TN);
-    for (int kb = 0; kb < blocks; ++kb) {
-      const int s = kb % S, use = kb / S;
-      wait_or_flag(full + 8 * s, use & 1, failed, p.err, kErrStageTimeout);
+      for (int i = issued > S ? issued - S : 0; i < issued; ++i) (void)phase_wait(full + 8 * (i % S), (i / S) & 1);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = F::idesc(128, TN);
+    const bool issuer = elect_one();
+    const uint32_t w_lo = desc_lo(w_at), a_lo = desc_lo(a_at), sf_lo = desc_lo(sf_at);
+    for (int i = 0; i < blocks; ++i) {
+      const int s = i % S;
+      phase_or_flag(full + 8 * s, (i / S) & 1, failed, p.err, kErrStageTimeout);
+      failed = __any_sync(0xffffffffu, failed);
       if (failed) break;
       tmem_fence_after();
-      const uint32_t sf = tmem + TN + s * 2 * C::SF_COLS;
-      const int bytes = p.row_bytes_used - kb * 128;
-      const int steps = bytes >= 128 ? 4 : (bytes + 31) / 32;
-      const int atoms = (steps + F::STEPS_PER_ATOM - 1) / F::STEPS_PER_ATOM;
-      for (int i = 0; i < atoms; ++i) {
-        scales_to_tmem<1>(sf + 4 * i, scales_desc(wsf_at(s) + 512 * i));
-        scales_to_tmem<1>(sf + C::SF_COLS + 4 * i, scales_desc(asf_at(s) + 512 * i));
+      if (issuer) {
+        const uint32_t sfs = sf_lo + s * (2 * C::SF_BYTES >> 4);
+        block_products_of<FMT, 1, 1>(p.row_bytes_used - (kb0 + i) * 128, tmem, tmem + TN + s * 2 * C::SF_COLS,
+                                     w_lo + s * (C::W_BYTES >> 4), a_lo + s * (C::A_BYTES >> 4), sfs,
+                                     sfs + (C::SF_BYTES >> 4), idesc, i > 0);
+        mma_commit<1>(empty + 8 * s);
       }
-      for (int j = 0; j < steps; ++j) {
-        const int i = j / F::STEPS_PER_ATOM;
-        mma_scaled<FMT, 1>(tmem, operand_desc(w_at(s) + 32 * j), operand_desc(a_at(s) + 32 * j),
-                        step_idesc<FMT>(idesc, j), sf + 4 * i, sf + C::SF_COLS + 4 * i,
-                        kb > 0 || j > 0);
-      }
-      mma_commit<1>(empty + 8 * s);
+      __syncwarp();
     }
-    mma_commit<1>(done);
-  } else if (warp >= 2) {
-    // warp w reads the TMEM lanes 32 (w % 4) ..: weight rows n0 + those
-    bool failed = false;
-    wait_or_flag(done, 0, failed, p.err, kErrStageTimeout);
+    if (issuer) mma_commit<1>(done);
+    __syncwarp();
+  }
+  // Warps 2..5 read the accumulator: warp w the TMEM lanes 32 (w % 4) .., that
+  // is the weight rows n0 + those.
+  const int row = 32 * (warp % 4) + lane;
+  const bool reader = warp >= 2;
+  const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
+  if (reader) {
+    phase_or_flag(done, 0, failed, p.err, kErrStageTimeout);
+    failed = __any_sync(0xffffffffu, failed);
     tmem_fence_after();
     grid_dep_launch_dependents();
-    const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
-    const int q = warp % 4;
-    const int64_t n = n0 + 32 * q + lane;
     for (int c = 0; c < TN; c += 16) {
       uint32_t r[16];
-      tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + c, r);
-      tmem_ld_wait();
+      tmem_ld16(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + c, r);
+      tmem_ld_wait(r);
+#pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int64_t m = m0 + c + j;
-        if (!failed && n < p.n && m < p.m)
-          p.out[m * p.out_row + n] =
-              (uint16_t)pack_bf16x2(__uint_as_float(r[j]) * scale, 0.f);
+        if (split == 1) {
+          const int64_t m = m0 + c + j;
+          if (!failed && n0 + row < p.n && m < p.m)
+            p.out[m * p.out_row + n0 + row] = (uint16_t)pack_bf16x2(__uint_as_float(r[j]) * scale, 0.f);
+        } else {
+          // the stages are free: every product that read them is complete
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)((c + j) * 128 + row) * 4u), "r"(r[j])
+                       : "memory");
+        }
       }
     }
     tmem_fence_before();
   }
   __syncwarp();
   __syncthreads();
+  if (split > 1) {
+    cluster_sync();
+    // every rank's threads take quadruples of output columns of some tokens;
+    // the loads of all parts are in flight together, their order of addition
+    // is that of the ranks
+    const int64_t left = p.m - m0;
+    const int quads = (left < TN ? (int)left : TN) * 32;
+    for (int i = rank * C::THREADS + (int)threadIdx.x; i < quads; i += split * C::THREADS) {
+      const uint32_t at = base + (uint32_t)i * 16u;
+      float4 part[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)
+        if (r < split)
+          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(part[r].x), "=f"(part[r].y), "=f"(part[r].z), "=f"(part[r].w)
+                       : "r"(map_rank(at, (uint32_t)r))
+                       : "memory");
+      float4 sum = part[0];
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r)
+        if (r < split) {
+          sum.x += part[r].x;
+          sum.y += part[r].y;
+          sum.z += part[r].z;
+          sum.w += part[r].w;
+        }
+      const int n = n0 + i % 32 * 4;
+      uint16_t* const o = p.out + (m0 + i / 32) * p.out_row + n;
+      const uint2 v = make_uint2(pack_bf16x2(sum.x * scale, sum.y * scale),
+                                 pack_bf16x2(sum.z * scale, sum.w * scale));
+      if (failed) continue;
+      if (n + 4 <= p.n) {
+        *reinterpret_cast<uint2*>(o) = v;
+      } else {
+        if (n < p.n) o[0] = (uint16_t)v.x;
+        if (n + 1 < p.n) o[1] = (uint16_t)(v.x >> 16);
+        if (n + 2 < p.n) o[2] = (uint16_t)v.y;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA ends while its part is being read
+  }
   if (warp == 1) {
     tmem_fence_after();
     tmem_free<1>(tmem, C::COLS);
@@ -325,9 +487,14 @@ __global__ void __launch_bounds__(192)
 // holds 128 tokens' rows, half of the weight rows (the instruction reads the
 // other half from the peer) and the scales of its tokens and of all 256
 // weight rows.  Persistent pairs walk the tiles; warp 0 loads, warp 1 of the
-// first CTA issues the MMAs of both, warps 4..11 drain the accumulator: to
-// bf16 in registers first, which frees it for the next tile, then through
-// shared memory to bulk tensor stores.
+// first CTA issues the MMAs of both, warps 4..11 drain the accumulator through
+// registers and shared memory to bulk tensor stores.
+//
+// Two accumulators of 256 columns and the scales do not fit TMEM's 512
+// columns, so the accumulators of successive tiles share 128: the first at
+// columns 0.., the second at 128..  A tile's shared columns are drained first,
+// and the next tile's products begin as soon as they are; the other half is
+// drained beside them.
 template <int FMT>
 struct WideCfg {
   using F = ProductFmt<FMT>;
@@ -339,9 +506,12 @@ struct WideCfg {
   static constexpr uint32_t OUT_BYTES = 32 * 128;  // one warp's 32 rows x 64 columns
   static constexpr int EPI_WARPS = 8;
   static constexpr uint32_t SMEM = STAGES * STAGE + EPI_WARPS * OUT_BYTES + 1024;
-  static constexpr int SF_COLS = F::ATOMS * 4;  // TMEM columns of 128 rows' scales
-  static constexpr int COLS = 512;
-  static_assert(TN + STAGES * 3 * SF_COLS <= COLS, "TMEM");
+  // TMEM: accumulators at 0 and 128, scales from 384 on, in a ring of SF_RING
+  // blocks (of all three row tiles)
+  static constexpr int COLS = 512, SF_AT = 384;
+  static constexpr int SF_COLS = 3 * F::ATOMS * 4;
+  static constexpr int SF_RING = (COLS - SF_AT) / SF_COLS < STAGES ? (COLS - SF_AT) / SF_COLS : STAGES;
+  static_assert(SF_RING >= 2, "TMEM");
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
 };
 
@@ -350,18 +520,18 @@ struct WideMaps {
 };
 
 struct TileWalk {
-  int64_t m_tiles, n_tiles;
+  int m_tiles, n_tiles;
 };
 // Tile `i` of the walk: bands of kBand token tiles, column by column within a
 // band, so that the pairs at work share weight rows and token rows in L2.
-constexpr int64_t kBand = 8;
-__device__ __forceinline__ void tile_at(const TileWalk& w, int64_t i, int64_t& mt, int64_t& nt) {
-  const int64_t band = i / (kBand * w.n_tiles);
-  const int64_t left = w.m_tiles - band * kBand;
-  const int64_t rows = left < kBand ? left : kBand;
-  const int64_t j = i - band * kBand * w.n_tiles;
-  mt = band * kBand + j % rows;
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_at(const TileWalk& w, int i, int& mt, int& nt) {
+  const int band = i / (kBand * w.n_tiles);
+  const int left = w.m_tiles - band * kBand;
+  const int rows = left < kBand ? left : kBand;
+  const int j = i - band * kBand * w.n_tiles;
   nt = j / rows;
+  mt = band * kBand + j - nt * rows;
 }
 
 template <int FMT>
@@ -370,19 +540,18 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
                                     const __grid_constant__ WideMaps maps) {
   using C = WideCfg<FMT>;
   using F = ProductFmt<FMT>;
-  constexpr int S = C::STAGES;
+  constexpr int S = C::STAGES, R = C::SF_RING;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long bars[2 * S + 2];
   __shared__ uint32_t tmem_slot;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * S, acc_full = empty + 8 * S,
                  acc_empty = acc_full + 8;
-  auto a_at = [&](int s) { return base + s * C::A_BYTES; };
-  auto w_at = [&](int s) { return base + S * C::A_BYTES + s * C::W_BYTES; };
+  const uint32_t a_at = base, w_at = base + S * C::A_BYTES;
   const uint32_t out_at = base + S * (C::A_BYTES + C::W_BYTES);  // 1024-byte aligned, as the swizzle wants
-  auto sf_at = [&](int s) { return out_at + C::EPI_WARPS * C::OUT_BYTES + s * 3 * C::SF_BYTES; };
+  const uint32_t sf_at = out_at + C::EPI_WARPS * C::OUT_BYTES;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
     mbar_init(acc_empty, 2 * C::EPI_WARPS);
@@ -393,9 +562,9 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
   __syncthreads();
   cluster_sync();
   tmem_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const int64_t tiles = walk.m_tiles * walk.n_tiles;
-  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
+  const int tiles = walk.m_tiles * walk.n_tiles;
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
   const int blocks = (p.row_bytes_used + 127) / 128;
   grid_dep_wait();
 
@@ -404,21 +573,22 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
     int s = 0;
     uint32_t use = 0, issued = 0;
     const int tiles_k = (int)p.group_tiles;
-    for (int64_t i = first; i < tiles && !failed; i += step) {
-      int64_t mt, nt;
+    for (int i = first; i < tiles && !failed; i += step) {
+      int mt, nt;
       tile_at(walk, i, mt, nt);
-      const int a_row = (int)(mt * 256 + rank * 128), w_row = (int)(nt * 256 + rank * 128);
+      const int a_row = mt * 256 + (int)rank * 128, w_row = nt * 256 + (int)rank * 128;
       for (int kb = 0; kb < blocks; ++kb) {
-        if (use > 0) wait_or_flag(empty + 8 * s, (use - 1) & 1, failed, p.err, kErrStageTimeout);
+        if (use > 0) phase_or_flag(empty + 8 * s, (use - 1) & 1, failed, p.err, kErrStageTimeout);
         if (failed) break;
         const uint32_t bar = full + 8 * s, bar0 = map_rank(bar, 0);
         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * C::STAGE);
         const int sf_row = kb * F::ATOMS;
-        tma_load_2d_pair(a_at(s), &maps.a, kb * 128, a_row, bar0);
-        tma_load_2d_pair(w_at(s), &maps.w, kb * 128, w_row, bar0);
-        tma_load_2d_pair(sf_at(s), &maps.a_sf, 0, a_row / 128 * tiles_k + sf_row, bar0);
-        tma_load_2d_pair(sf_at(s) + C::SF_BYTES, &maps.w_sf, 0, (int)nt * 2 * tiles_k + sf_row, bar0);
-        tma_load_2d_pair(sf_at(s) + 2 * C::SF_BYTES, &maps.w_sf, 0, ((int)nt * 2 + 1) * tiles_k + sf_row, bar0);
+        const uint32_t sf = sf_at + s * 3 * C::SF_BYTES;
+        tma_load_2d_pair(a_at + s * C::A_BYTES, &maps.a, kb * 128, a_row, bar0);
+        tma_load_2d_pair(w_at + s * C::W_BYTES, &maps.w, kb * 128, w_row, bar0);
+        tma_load_2d_pair(sf, &maps.a_sf, 0, a_row / 128 * tiles_k + sf_row, bar0);
+        tma_load_2d_pair(sf + C::SF_BYTES, &maps.w_sf, 0, nt * 2 * tiles_k + sf_row, bar0);
+        tma_load_2d_pair(sf + 2 * C::SF_BYTES, &maps.w_sf, 0, (nt * 2 + 1) * tiles_k + sf_row, bar0);
         ++issued;
         if (++s == S) {
           s = 0;
@@ -428,92 +598,102 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
     }
     if (failed && rank == 0)  // copies still in flight (the peer's too) land before the CTAs end
       for (uint32_t b = issued > S ? issued - S : 0; b < issued; ++b)
-        (void)mbar_wait_bounded(full + 8 * (b % S), (b / S) & 1);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+        (void)phase_wait(full + 8 * (b % S), (b / S) & 1);
+  } else if (warp == 1 && rank == 0) {
     bool failed = false;
-    int s = 0;
-    uint32_t use = 0, tile = 0;
+    int s = 0, ring = 0, ring_s = 0;  // stage, scale slot, the stage that last used the slot
+    uint32_t use = 0, tile = 0, count = 0, ring_use = 0;
     constexpr uint32_t idesc = F::idesc(256, 256);
-    for (int64_t i = first; i < tiles && !failed; i += step, ++tile) {
+    const bool issuer = elect_one();
+    const uint32_t a_lo = desc_lo(a_at), w_lo = desc_lo(w_at), sf_lo = desc_lo(sf_at);
+    for (int i = first; i < tiles && !failed; i += step, ++tile) {
       if (tile > 0)
-        wait_or_flag_cluster(acc_empty, (tile - 1) & 1, failed, p.err, kErrExchangeTimeout);
-      for (int kb = 0; kb < blocks && !failed; ++kb) {
-        wait_or_flag(full + 8 * s, use & 1, failed, p.err, kErrStageTimeout);
+        phase_or_flag<true>(acc_empty, (tile - 1) & 1, failed, p.err, kErrExchangeTimeout);
+      const uint32_t acc = tmem + (tile & 1) * 128;
+      for (int kb = 0; kb < blocks; ++kb) {
+        phase_or_flag(full + 8 * s, use & 1, failed, p.err, kErrStageTimeout);
+        if constexpr (R < S) {  // the products that read this slot's scales are complete
+          if (count >= R) {
+            phase_or_flag(empty + 8 * ring_s, ring_use & 1, failed, p.err, kErrStageTimeout);
+            if (++ring_s == S) {
+              ring_s = 0;
+              ++ring_use;
+            }
+          }
+          ++count;
+        }
+        failed = __any_sync(0xffffffffu, failed);
         if (failed) break;
         tmem_fence_after();
-        const uint32_t sf = tmem + C::TN + s * 3 * C::SF_COLS;
-        const int bytes = p.row_bytes_used - kb * 128;
-        const int steps = bytes >= 128 ? 4 : (bytes + 31) / 32;
-        const int atoms = (steps + F::STEPS_PER_ATOM - 1) / F::STEPS_PER_ATOM;
-        for (int t = 0; t < atoms; ++t) {
-          // the token scales, and beside each other those of both halves of the weight rows
-          scales_to_tmem<2>(sf + 4 * t, scales_desc(sf_at(s) + 512 * t));
-          scales_to_tmem<2>(sf + C::SF_COLS + 8 * t, scales_desc(sf_at(s) + C::SF_BYTES + 512 * t));
-          scales_to_tmem<2>(sf + C::SF_COLS + 8 * t + 4, scales_desc(sf_at(s) + 2 * C::SF_BYTES + 512 * t));
+        if (issuer) {
+          const uint32_t sfs = sf_lo + s * (3 * C::SF_BYTES >> 4);
+          block_products_of<FMT, 2, 2>(p.row_bytes_used - kb * 128, acc, tmem + C::SF_AT + ring * C::SF_COLS,
+                                       a_lo + s * (C::A_BYTES >> 4), w_lo + s * (C::W_BYTES >> 4), sfs,
+                                       sfs + (C::SF_BYTES >> 4), idesc, kb > 0);
+          mma_commit<2>(empty + 8 * s);
         }
-        for (int j = 0; j < steps; ++j) {
-          const int t = j / F::STEPS_PER_ATOM;
-          mma_scaled<FMT, 2>(tmem, operand_desc(a_at(s) + 32 * j), operand_desc(w_at(s) + 32 * j),
-                             step_idesc<FMT>(idesc, j), sf + 4 * t, sf + C::SF_COLS + 8 * t,
-                             kb > 0 || j > 0);
-        }
-        mma_commit<2>(empty + 8 * s);
+        __syncwarp();
+        if (++ring == R) ring = 0;
         if (++s == S) {
           s = 0;
           ++use;
         }
       }
-      mma_commit<2>(acc_full);
+      if (issuer) mma_commit<2>(acc_full);
+      __syncwarp();
     }
-    if (failed) (void)mbar_wait_bounded(acc_full, (tile - 1) & 1);
+    if (failed) (void)phase_wait(acc_full, (tile - 1) & 1);
   } else if (warp >= 4) {
     bool failed = false;
     uint32_t tile = 0;
     const int q = warp % 4, half = (warp - 4) / 4;
     const uint32_t stage = out_at + (uint32_t)(warp - 4) * C::OUT_BYTES;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
     const uint32_t release = map_rank(acc_empty, 0);
     // a bulk tensor store ends on a 16-byte boundary: the columns behind the
     // last one are stored one by one
-    const int64_t whole = p.n / 8 * 8;
-    for (int64_t i = first; i < tiles && !failed; i += step, ++tile) {
-      int64_t mt, nt;
+    const int whole = (int)(p.n / 8 * 8);
+    for (int i = first; i < tiles && !failed; i += step, ++tile) {
+      int mt, nt;
       tile_at(walk, i, mt, nt);
-      wait_or_flag(acc_full, tile & 1, failed, p.err, kErrStageTimeout);
+      phase_or_flag(acc_full, tile & 1, failed, p.err, kErrStageTimeout);
       failed = __any_sync(0xffffffffu, failed);
       tmem_fence_after();
       if (i + step >= tiles) grid_dep_launch_dependents();
-      uint32_t v[64];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t r[16];
-        tmem_ld16(lanes + 16 * c, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[8 * c + k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
-      }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(release);
-      const int row = (int)(mt * 256 + rank * 128 + 32 * q);
+      const int64_t row = (int64_t)mt * 256 + rank * 128 + 32 * q;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t col = nt * 256 + 128 * half + 64 * h;
+        // 64 of the tile's columns: first of the 128 that the accumulators
+        // share (the upper of the first, the lower of the second)
+        const int local = ((tile & 1) == (h == 0 ? 0u : 1u) ? 128 : 0) + 64 * half;
+        uint32_t r[64];
+        tmem_ld64(lanes + (tile & 1) * 128 + local, r);
+        tmem_ld_wait(r);
+        if (h == 0) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(release);
+        }
+        const int col = nt * 256 + local;
         if (lane == 0) bulk_wait_read();
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * scale,
+                               __uint_as_float(r[8 * k + 2 * e + 1]) * scale);
           const uint32_t at = stage + lane * 128 + ((k ^ (lane & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[32 * h + 4 * k]),
-                       "r"(v[32 * h + 4 * k + 1]), "r"(v[32 * h + 4 * k + 2]), "r"(v[32 * h + 4 * k + 3])
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                       "r"(v[3])
                        : "memory");
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && !failed && row < p.m && col < whole) {
-          tma_store_2d(&maps.out, (int)col, row, stage);
+          tma_store_2d(&maps.out, col, (int)row, stage);
           bulk_commit();
         }
         if (whole >= col && whole < col + 64 && whole < p.n && !failed && row + lane < p.m) {
@@ -524,7 +704,9 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
             p.out[(row + lane) * p.out_row + whole + k] = e;
           }
         }
+        __syncwarp();
       }
+      tmem_fence_before();
     }
     if (lane == 0) bulk_wait();
   }
