@@ -60,23 +60,6 @@ cudaError_t scales_map(const attn_res_mx_t& x, uint32_t tiles, CUtensorMap* map)
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Of the result's columns up to the last 16-byte boundary: boxes of 64 columns
-// x 32 rows, 128-byte swizzle (at least one boundary, which then no store uses).
-cudaError_t out_map(const ProductCall& c, CUtensorMap* map) {
-  EncodeTiled enc;
-  cudaError_t e = encode_tiled(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t whole = (cuuint64_t)(c.w->rows / 8 * 8);
-  const cuuint64_t dim[2] = {whole ? whole : 8, (cuuint64_t)c.a->rows};
-  const cuuint64_t stride[1] = {(cuuint64_t)c.out_row * 2};
-  const cuuint32_t box[2] = {64, 32};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.out, dim, stride, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int FMT>
 ProductParams params(const ProductCall& c) {
   ProductParams p = {};
@@ -147,19 +130,18 @@ cudaError_t launch_narrow(const ProductCall& c) {
   return cudaLaunchKernelEx(&l.cfg, kern, p, map_a, map_w);
 }
 
-template <int FMT>
+template <int FMT, int HALVES>
 cudaError_t launch_wide(const ProductCall& c) {
-  using C = WideCfg<FMT>;
-  void (*kern)(ProductParams, TileWalk, WideMaps) = attn_res_mx_product_wide_kernel<FMT>;
+  using C = WideCfg<FMT, HALVES>;
+  void (*kern)(ProductParams, TileWalk, WideMaps) = attn_res_mx_product_wide_kernel<FMT, HALVES>;
   static std::atomic<uint64_t> enabled{0};
   static std::atomic<int> pairs_of[64];
   cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
   WideMaps maps;
   if (e == cudaSuccess) e = operand_map(*c.a, 128, &maps.a);
-  if (e == cudaSuccess) e = operand_map(*c.w, 128, &maps.w);
+  if (e == cudaSuccess) e = operand_map(*c.w, C::HN / 2, &maps.w);
   if (e == cudaSuccess) e = scales_map(*c.a, C::F::ATOMS, &maps.a_sf);
   if (e == cudaSuccess) e = scales_map(*c.w, C::F::ATOMS, &maps.w_sf);
-  if (e == cudaSuccess) e = out_map(c, &maps.out);
   if (e != cudaSuccess) return e;
   const ProductParams p = params<FMT>(c);
   const int64_t m_tiles = (p.m + C::TM - 1) / C::TM, n_tiles = (p.n + C::TN - 1) / C::TN;
@@ -178,6 +160,16 @@ cudaError_t launch_wide(const ProductCall& c) {
   return cudaLaunchKernelEx(&l.cfg, kern, p, walk, maps);
 }
 
+// The forms' time in units of 10 ns, for the choice between them.  Measured on
+// GB300 (mxfp4, 512..8192 tokens x 7168..16384 columns x 2048..8192): a pair
+// takes 1.1 us and 0.32 us for each 128-byte block of K for a tile of 256
+// columns, 2.5 us and 0.40 us for one of 384; 76 pairs work at once.
+int64_t wide_cost(const ProductCall& c, int64_t blocks, int tile_columns) {
+  const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + tile_columns - 1) / tile_columns);
+  const int64_t waves = (tiles + 75) / 76;
+  return waves * (tile_columns == 256 ? 110 + 32 * blocks : 250 + 40 * blocks);
+}
+
 template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
   static const int wide = getenv("WIDE") ? atoi(getenv("WIDE")) : 256;
@@ -185,7 +177,10 @@ cudaError_t launch_format(const ProductCall& c) {
   if (c.a->rows <= 32) return launch_narrow<FMT, 32>(c);
   if (c.a->rows <= 64) return launch_narrow<FMT, 64>(c);
   if (c.a->rows <= wide) return launch_narrow<FMT, 128>(c);
-  return launch_wide<FMT>(c);
+  const int64_t blocks = (c.a->cols * mx_bits(FMT) / 8 + 127) / 128;
+  static const int hv = getenv("HV") ? atoi(getenv("HV")) : 0;
+  if (hv ? hv == 2 : wide_cost(c, blocks, 384) < wide_cost(c, blocks, 256)) return launch_wide<FMT, 2>(c);
+  return launch_wide<FMT, 1>(c);
 }
 
 }  // namespace

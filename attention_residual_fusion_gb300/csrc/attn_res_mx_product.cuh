@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "attn_res_mx.cuh"
 
 namespace attn_res_dev {
@@ -27,14 +29,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // An arrival that orders nothing in shared or global memory: it tells that
 // this thread's TMEM loads are complete (they are: tcgen05.wait::ld has
 // returned, and tcgen05.fence::before_thread_sync keeps them before it).  With
@@ -225,14 +219,15 @@ __device__ __forceinline__ uint32_t step_idesc(uint32_t idesc, int j) {
   return idesc | id << 4 | id << 29;
 }
 
-// What the tensor cores do with one 128-byte block of K: scales to TMEM, then
-// `STEPS` products of 32 bytes.  P is the operand on the M side (128 rows a
-// CTA), Q the one on the N side, whose scales come in QT tiles of 128 rows.
-// Issued by one thread; all addresses are its first CTA's.
+// The tensor cores' work on one 128-byte block of K, issued by one thread;
+// addresses are its first CTA's.  P is the operand on the instruction's M side
+// (128 rows a CTA), Q the one on its N side, whose scales come in QT tiles of
+// 128 rows.  STEPS: the block's 32-byte steps, 4 but for the last block.
+//
+// The scales, to TMEM from column `sf` on: P's group tiles, then Q's, the row
+// tiles of one group tile side by side.
 template <int FMT, int G, int QT, int STEPS>
-__device__ __forceinline__ void block_products(uint32_t acc, uint32_t sf, uint32_t p_lo, uint32_t q_lo,
-                                               uint32_t psf_lo, uint32_t qsf_lo, uint32_t idesc,
-                                               uint32_t accumulate) {
+__device__ __forceinline__ void block_scales(uint32_t sf, uint32_t psf_lo, uint32_t qsf_lo) {
   using F = ProductFmt<FMT>;
   constexpr int ATOMS = (STEPS + F::STEPS_PER_ATOM - 1) / F::STEPS_PER_ATOM;
   constexpr uint32_t TILE = 512 >> 4;  // a scale tile, in descriptor units
@@ -240,31 +235,32 @@ __device__ __forceinline__ void block_products(uint32_t acc, uint32_t sf, uint32
   for (int t = 0; t < ATOMS; ++t) {
     scales_to_tmem<G>(sf + 4 * t, desc_of(psf_lo + TILE * t, kScalesHi));
 #pragma unroll
-    for (int h = 0; h < QT; ++h)  // the row tiles of one group tile side by side
+    for (int h = 0; h < QT; ++h)
       scales_to_tmem<G>(sf + F::ATOMS * 4 + 4 * (QT * t + h),
                         desc_of(qsf_lo + TILE * (F::ATOMS * h + t), kScalesHi));
   }
+}
+// The products with Q rows whose scales begin `q_col` columns into Q's.
+template <int FMT, int G, int QT, int STEPS>
+__device__ __forceinline__ void block_steps(uint32_t acc, uint32_t sf, uint32_t q_col, uint32_t p_lo,
+                                            uint32_t q_lo, uint32_t idesc, uint32_t accumulate) {
+  using F = ProductFmt<FMT>;
 #pragma unroll
   for (int j = 0; j < STEPS; ++j) {
     const int t = j / F::STEPS_PER_ATOM;
     mma_scaled<FMT, G>(acc, desc_of(p_lo + 2 * j, kOperandHi), desc_of(q_lo + 2 * j, kOperandHi),
-                       step_idesc<FMT>(idesc, j), sf + 4 * t, sf + F::ATOMS * 4 + 4 * QT * t,
+                       step_idesc<FMT>(idesc, j), sf + 4 * t, sf + F::ATOMS * 4 + 4 * QT * t + q_col,
                        j > 0 ? 1u : accumulate);
   }
 }
-// The same for a block of `bytes` <= 128 bytes.
-template <int FMT, int G, int QT>
-__device__ __forceinline__ void block_products_of(int bytes, uint32_t acc, uint32_t sf, uint32_t p_lo,
-                                                  uint32_t q_lo, uint32_t psf_lo, uint32_t qsf_lo,
-                                                  uint32_t idesc, uint32_t accumulate) {
-  if (bytes > 96)
-    block_products<FMT, G, QT, 4>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
-  else if (bytes > 64)
-    block_products<FMT, G, QT, 3>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
-  else if (bytes > 32)
-    block_products<FMT, G, QT, 2>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
-  else
-    block_products<FMT, G, QT, 1>(acc, sf, p_lo, q_lo, psf_lo, qsf_lo, idesc, accumulate);
+// f(integral constant) with the steps of a block of `bytes` bytes (any number
+// from 128 on is a whole block).
+template <class Fn>
+__device__ __forceinline__ void with_steps(int bytes, Fn f) {
+  if (bytes > 96) f(std::integral_constant<int, 4>());
+  else if (bytes > 64) f(std::integral_constant<int, 3>());
+  else if (bytes > 32) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 1>());
 }
 
 struct ProductParams {
@@ -392,9 +388,12 @@ __global__ void __launch_bounds__(192)
       tmem_fence_after();
       if (issuer) {
         const uint32_t sfs = sf_lo + s * (2 * C::SF_BYTES >> 4);
-        block_products_of<FMT, 1, 1>(p.row_bytes_used - (kb0 + i) * 128, tmem, tmem + TN + s * 2 * C::SF_COLS,
-                                     w_lo + s * (C::W_BYTES >> 4), a_lo + s * (C::A_BYTES >> 4), sfs,
-                                     sfs + (C::SF_BYTES >> 4), idesc, i > 0);
+        const uint32_t sf = tmem + TN + s * 2 * C::SF_COLS;
+        with_steps(p.row_bytes_used - (kb0 + i) * 128, [&](auto steps) {
+          block_scales<FMT, 1, 1, decltype(steps)::value>(sf, sfs, sfs + (C::SF_BYTES >> 4));
+          block_steps<FMT, 1, 1, decltype(steps)::value>(tmem, sf, 0, w_lo + s * (C::W_BYTES >> 4), a_lo + s * (C::A_BYTES >> 4),
+                                          idesc, i > 0);
+        });
         mma_commit<1>(empty + 8 * s);
       }
       __syncwarp();
@@ -481,42 +480,48 @@ __global__ void __launch_bounds__(192)
   }
 }
 
-// ---- many tokens: CTA pairs, 256 x 256 tiles ------------------------------------------------
+// ---- many tokens: CTA pairs ----------------------------------------------------------------
 //
-// A pair of CTAs (cta_group::2) makes 256 tokens x 256 output columns: each
+// A pair of CTAs (cta_group::2) makes 256 tokens x TN output columns: each
 // holds 128 tokens' rows, half of the weight rows (the instruction reads the
-// other half from the peer) and the scales of its tokens and of all 256
-// weight rows.  Persistent pairs walk the tiles; warp 0 loads, warp 1 of the
-// first CTA issues the MMAs of both, warps 4..11 drain the accumulator through
-// registers and shared memory to bulk tensor stores.
+// other half from the peer) and the scales of its tokens and of all TN weight
+// rows.  Persistent pairs walk the tiles; warp 0 loads, warp 1 of the first
+// CTA issues the MMAs of both, warps 4..11 drain the accumulators through
+// registers to global memory.
 //
-// Two accumulators of 256 columns and the scales do not fit TMEM's 512
-// columns, so the accumulators of successive tiles share 128: the first at
-// columns 0.., the second at 128..  A tile's shared columns are drained first,
-// and the next tile's products begin as soon as they are; the other half is
-// drained beside them.
-template <int FMT>
+// What bounds a tile is what an SM takes in (measured: 60 bytes a clock of
+// the 64 its port has) more than the tensor cores, so wide tiles:
+//   HALVES = 2: 384 columns, as two instructions of 192 with an accumulator
+//     each.  The first half of the next tile's products waits only for the
+//     first accumulator's draining.
+//   HALVES = 1: 256 columns, for products that make too few of the wide ones.
+//     Two accumulators of 256 columns and the scales do not fit TMEM's 512
+//     columns, so those of successive tiles share 128: the first at columns
+//     0.., the second at 128..  A tile's shared columns are drained first, and
+//     the next tile's products begin as soon as they are.
+template <int FMT, int HALVES>
 struct WideCfg {
   using F = ProductFmt<FMT>;
-  static constexpr int TM = 256, TN = 256;
-  static constexpr uint32_t A_BYTES = 128 * 128, W_BYTES = 128 * 128;
+  static constexpr int HN = HALVES == 1 ? 256 : 192;  // columns of an instruction
+  static constexpr int TM = 256, TN = HN * HALVES;
+  static constexpr int QT = TN / 128;  // scale tiles of 128 weight rows
+  static constexpr uint32_t A_BYTES = 128 * 128, W_BYTES = TN / 2 * 128, WH_BYTES = HN / 2 * 128;
   static constexpr uint32_t SF_BYTES = F::ATOMS * 512;  // of 128 rows
-  static constexpr uint32_t STAGE = A_BYTES + W_BYTES + 3 * SF_BYTES;
-  static constexpr int STAGES = 5;
-  static constexpr uint32_t OUT_BYTES = 32 * 128;  // one warp's 32 rows x 64 columns
-  static constexpr int EPI_WARPS = 8;
-  static constexpr uint32_t SMEM = STAGES * STAGE + EPI_WARPS * OUT_BYTES + 1024;
-  // TMEM: accumulators at 0 and 128, scales from 384 on, in a ring of SF_RING
-  // blocks (of all three row tiles)
+  static constexpr uint32_t STAGE = A_BYTES + W_BYTES + (1 + QT) * SF_BYTES;
+  static constexpr int STAGES = (226 * 1024 - 1024) / STAGE;
+  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
+  // TMEM: accumulators, then the scales in a ring of SF_RING blocks
   static constexpr int COLS = 512, SF_AT = 384;
-  static constexpr int SF_COLS = 3 * F::ATOMS * 4;
+  static constexpr int ACC_STEP = HALVES == 1 ? 128 : 192;  // between the two accumulators
+  static constexpr int SF_COLS = (1 + QT) * F::ATOMS * 4;
   static constexpr int SF_RING = (COLS - SF_AT) / SF_COLS < STAGES ? (COLS - SF_AT) / SF_COLS : STAGES;
-  static_assert(SF_RING >= 2, "TMEM");
+  static_assert(SF_RING >= 2 && SMEM <= 227 * 1024, "TMEM and shared memory");
+  static constexpr int EPI_WARPS = HALVES == 1 ? 8 : 12;  // four for each 64 columns of an accumulator
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
 };
 
 struct WideMaps {
-  CUtensorMap a, w, a_sf, w_sf, out;
+  CUtensorMap a, w, a_sf, w_sf;
 };
 
 struct TileWalk {
@@ -534,27 +539,59 @@ __device__ __forceinline__ void tile_at(const TileWalk& w, int i, int& mt, int& 
   mt = band * kBand + j - nt * rows;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
+// Stores 64 fp32 columns (from `col` on) of a lane's row as bf16, straight from
+// its registers: 32 bytes, a whole sector, at a time where the rows lie on
+// 32-byte boundaries.  (Through shared memory and bulk tensor stores the same
+// bytes passed shared memory twice, whose bandwidth the operands need.)
+__device__ __forceinline__ void store_row64(const ProductParams& p, const uint32_t (&r)[64], float scale,
+                                            int64_t row, int col, bool wide) {
+  uint16_t* const o = p.out + row * p.out_row + col;
+  const int left = (int)p.n - col;  // columns that exist
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = pack_bf16x2(__uint_as_float(r[16 * k + 2 * e]) * scale, __uint_as_float(r[16 * k + 2 * e + 1]) * scale);
+    uint16_t* const at = o + 16 * k;
+    if (left >= 16 * k + 16) {
+      if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+      } else {
+        st_row(at, make_uint4(v[0], v[1], v[2], v[3]));
+        st_row(at + 8, make_uint4(v[4], v[5], v[6], v[7]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (16 * k + e < left) at[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+    }
+  }
+}
+
+template <int FMT, int HALVES>
+__global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
     attn_res_mx_product_wide_kernel(const ProductParams p, const TileWalk walk,
                                     const __grid_constant__ WideMaps maps) {
-  using C = WideCfg<FMT>;
+  using C = WideCfg<FMT, HALVES>;
   using F = ProductFmt<FMT>;
   constexpr int S = C::STAGES, R = C::SF_RING;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long bars[2 * S + 2];
+  __shared__ __align__(8) unsigned long long bars[2 * S + 2 * HALVES + 1];
   __shared__ uint32_t tmem_slot;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * S, acc_full = empty + 8 * S,
-                 acc_empty = acc_full + 8;
+                 acc_empty = acc_full + 8 * HALVES, drained = acc_empty + 8 * HALVES;
   const uint32_t a_at = base, w_at = base + S * C::A_BYTES;
-  const uint32_t out_at = base + S * (C::A_BYTES + C::W_BYTES);  // 1024-byte aligned, as the swizzle wants
-  const uint32_t sf_at = out_at + C::EPI_WARPS * C::OUT_BYTES;
+  const uint32_t sf_at = base + S * (C::A_BYTES + C::W_BYTES);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
-    mbar_init(acc_empty, 2 * C::EPI_WARPS);
+    for (int i = 0; i < 2 * S + HALVES; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < HALVES; ++i) mbar_init(acc_empty + 8 * i, 2 * C::EPI_WARPS);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<2>(smem_addr(&tmem_slot), C::COLS);
@@ -576,19 +613,22 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
     for (int i = first; i < tiles && !failed; i += step) {
       int mt, nt;
       tile_at(walk, i, mt, nt);
-      const int a_row = mt * 256 + (int)rank * 128, w_row = nt * 256 + (int)rank * 128;
+      const int a_row = mt * C::TM + (int)rank * 128, w_row = nt * C::TN + (int)rank * (C::HN / 2);
       for (int kb = 0; kb < blocks; ++kb) {
         if (use > 0) phase_or_flag(empty + 8 * s, (use - 1) & 1, failed, p.err, kErrStageTimeout);
         if (failed) break;
         const uint32_t bar = full + 8 * s, bar0 = map_rank(bar, 0);
         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * C::STAGE);
         const int sf_row = kb * F::ATOMS;
-        const uint32_t sf = sf_at + s * 3 * C::SF_BYTES;
+        const uint32_t sf = sf_at + s * (1 + C::QT) * C::SF_BYTES;
         tma_load_2d_pair(a_at + s * C::A_BYTES, &maps.a, kb * 128, a_row, bar0);
-        tma_load_2d_pair(w_at + s * C::W_BYTES, &maps.w, kb * 128, w_row, bar0);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+          tma_load_2d_pair(w_at + s * C::W_BYTES + h * C::WH_BYTES, &maps.w, kb * 128, w_row + h * C::HN, bar0);
         tma_load_2d_pair(sf, &maps.a_sf, 0, a_row / 128 * tiles_k + sf_row, bar0);
-        tma_load_2d_pair(sf + C::SF_BYTES, &maps.w_sf, 0, nt * 2 * tiles_k + sf_row, bar0);
-        tma_load_2d_pair(sf + 2 * C::SF_BYTES, &maps.w_sf, 0, (nt * 2 + 1) * tiles_k + sf_row, bar0);
+#pragma unroll
+        for (int h = 0; h < C::QT; ++h)
+          tma_load_2d_pair(sf + (1 + h) * C::SF_BYTES, &maps.w_sf, 0, (nt * C::QT + h) * tiles_k + sf_row, bar0);
         ++issued;
         if (++s == S) {
           s = 0;
@@ -603,13 +643,11 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
     bool failed = false;
     int s = 0, ring = 0, ring_s = 0;  // stage, scale slot, the stage that last used the slot
     uint32_t use = 0, tile = 0, count = 0, ring_use = 0;
-    constexpr uint32_t idesc = F::idesc(256, 256);
+    constexpr uint32_t idesc = F::idesc(256, C::HN);
     const bool issuer = elect_one();
     const uint32_t a_lo = desc_lo(a_at), w_lo = desc_lo(w_at), sf_lo = desc_lo(sf_at);
     for (int i = first; i < tiles && !failed; i += step, ++tile) {
-      if (tile > 0)
-        phase_or_flag<true>(acc_empty, (tile - 1) & 1, failed, p.err, kErrExchangeTimeout);
-      const uint32_t acc = tmem + (tile & 1) * 128;
+      const uint32_t acc = HALVES == 1 ? tmem + (tile & 1) * C::ACC_STEP : tmem;
       for (int kb = 0; kb < blocks; ++kb) {
         phase_or_flag(full + 8 * s, use & 1, failed, p.err, kErrStageTimeout);
         if constexpr (R < S) {  // the products that read this slot's scales are complete
@@ -622,16 +660,28 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
           }
           ++count;
         }
-        failed = __any_sync(0xffffffffu, failed);
-        if (failed) break;
-        tmem_fence_after();
-        if (issuer) {
-          const uint32_t sfs = sf_lo + s * (3 * C::SF_BYTES >> 4);
-          block_products_of<FMT, 2, 2>(p.row_bytes_used - kb * 128, acc, tmem + C::SF_AT + ring * C::SF_COLS,
-                                       a_lo + s * (C::A_BYTES >> 4), w_lo + s * (C::W_BYTES >> 4), sfs,
-                                       sfs + (C::SF_BYTES >> 4), idesc, kb > 0);
-          mma_commit<2>(empty + 8 * s);
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+          if (kb == 0 && tile > 0)
+            phase_or_flag<true>(acc_empty + 8 * h, (tile - 1) & 1, failed, p.err, kErrExchangeTimeout);
+          if (h == 0 || kb == 0) {
+            failed = __any_sync(0xffffffffu, failed);
+            tmem_fence_after();
+          }
+          if (issuer && !failed) {
+            const uint32_t sfs = sf_lo + s * ((1 + C::QT) * C::SF_BYTES >> 4);
+            const uint32_t sf = tmem + C::SF_AT + ring * C::SF_COLS;
+            with_steps(p.row_bytes_used - kb * 128, [&](auto steps) {
+              if (h == 0) block_scales<FMT, 2, C::QT, decltype(steps)::value>(sf, sfs, sfs + (C::SF_BYTES >> 4));
+              block_steps<FMT, 2, C::QT, decltype(steps)::value>(acc + h * C::ACC_STEP, sf, h * (C::HN / 32),
+                                                  a_lo + s * (C::A_BYTES >> 4),
+                                                  w_lo + (s * C::W_BYTES + h * C::WH_BYTES >> 4), idesc, kb > 0);
+            });
+            if (kb == blocks - 1) mma_commit<2>(acc_full + 8 * h);
+          }
         }
+        if (failed) break;
+        if (issuer) mma_commit<2>(empty + 8 * s);
         __syncwarp();
         if (++ring == R) ring = 0;
         if (++s == S) {
@@ -639,76 +689,44 @@ __global__ void __launch_bounds__(WideCfg<FMT>::THREADS, 1)
           ++use;
         }
       }
-      if (issuer) mma_commit<2>(acc_full);
-      __syncwarp();
     }
-    if (failed) (void)phase_wait(acc_full, (tile - 1) & 1);
+    if (failed) {  // what was issued ends before the CTAs do
+      if (issuer) mma_commit<2>(drained);
+      __syncwarp();
+      (void)phase_wait(drained, 0);
+    }
   } else if (warp >= 4) {
     bool failed = false;
     uint32_t tile = 0;
-    const int q = warp % 4, half = (warp - 4) / 4;
-    const uint32_t stage = out_at + (uint32_t)(warp - 4) * C::OUT_BYTES;
+    const int q = warp % 4, part = (warp - 4) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
-    const uint32_t release = map_rank(acc_empty, 0);
-    // a bulk tensor store ends on a 16-byte boundary: the columns behind the
-    // last one are stored one by one
-    const int whole = (int)(p.n / 8 * 8);
+    const bool wide = p.out_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     for (int i = first; i < tiles && !failed; i += step, ++tile) {
       int mt, nt;
       tile_at(walk, i, mt, nt);
-      phase_or_flag(acc_full, tile & 1, failed, p.err, kErrStageTimeout);
-      failed = __any_sync(0xffffffffu, failed);
-      tmem_fence_after();
-      if (i + step >= tiles) grid_dep_launch_dependents();
-      const int64_t row = (int64_t)mt * 256 + rank * 128 + 32 * q;
+      const int64_t row = (int64_t)mt * C::TM + rank * 128 + 32 * q + lane;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        // 64 of the tile's columns: first of the 128 that the accumulators
-        // share (the upper of the first, the lower of the second)
-        const int local = ((tile & 1) == (h == 0 ? 0u : 1u) ? 128 : 0) + 64 * half;
+        if (HALVES == 2 || h == 0) {
+          phase_or_flag(acc_full + 8 * h, tile & 1, failed, p.err, kErrStageTimeout);
+          failed = __any_sync(0xffffffffu, failed);
+          tmem_fence_after();
+        }
+        // 64 columns: of accumulator h, or first of the 128 that successive
+        // accumulators share (the upper of the first, the lower of the second)
+        const int local = HALVES == 2 ? h * C::HN + 64 * part
+                                      : ((tile & 1) == (h == 0 ? 0u : 1u) ? 128 : 0) + 64 * part;
         uint32_t r[64];
-        tmem_ld64(lanes + (tile & 1) * 128 + local, r);
+        tmem_ld64(lanes + (HALVES == 2 ? 0 : (tile & 1) * C::ACC_STEP) + local, r);
         tmem_ld_wait(r);
-        if (h == 0) {
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(release);
-        }
-        const int col = nt * 256 + local;
-        if (lane == 0) bulk_wait_read();
+        tmem_fence_before();
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * scale,
-                               __uint_as_float(r[8 * k + 2 * e + 1]) * scale);
-          const uint32_t at = stage + lane * 128 + ((k ^ (lane & 7)) * 16);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                       "r"(v[3])
-                       : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && !failed && row < p.m && col < whole) {
-          tma_store_2d(&maps.out, col, (int)row, stage);
-          bulk_commit();
-        }
-        if (whole >= col && whole < col + 64 && whole < p.n && !failed && row + lane < p.m) {
-          const uint32_t at = stage + lane * 128 + ((((uint32_t)(whole - col) >> 3) ^ (lane & 7)) * 16);
-          for (int k = 0; whole + k < p.n; ++k) {
-            uint16_t e;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(at + 2 * k) : "memory");
-            p.out[(row + lane) * p.out_row + whole + k] = e;
-          }
-        }
-        __syncwarp();
+        if ((HALVES == 2 || h == 0) && lane == 0) mbar_arrive_remote(map_rank(acc_empty + 8 * h, 0));
+        if (!failed && row < p.m) store_row64(p, r, scale, row, nt * C::TN + local, wide);
       }
-      tmem_fence_before();
+      if (i + step >= tiles) grid_dep_launch_dependents();
     }
-    if (lane == 0) bulk_wait();
   }
   __syncwarp();
   __syncthreads();
