@@ -1,6 +1,4 @@
 // attn_res_mx_product.cu -- launches of the microscaled product.
-#include <cstdio>
-#include <cstdlib>
 #include "attn_res_mx_host.cuh"
 
 namespace attn_res_host {
@@ -108,6 +106,21 @@ struct Attributes {
   Attributes(const Attributes&) = delete;
 };
 
+// CTAs that share a tile's K in the narrow form: two CTAs an SM (of 152) if
+// that fills at least three quarters of them, else one (so that no SM has twice
+// the work of another); at most 6 (clusters of 8 measured slower than of 4..6
+// wherever they fit: 128 tokens x 2048 x 4096 9.3 us against 7.6, 64 x 4096 x
+// 7168 8.8 against 7.4) and a block of K each.
+int64_t narrow_split(int64_t tiles, int64_t blocks) {
+  auto per_sm = [&](int64_t ctas) {
+    const int64_t s = ctas / tiles;
+    return s > 6 ? 6 : s < 1 ? 1 : s;
+  };
+  int64_t s = per_sm(304);
+  if (s * tiles < 228) s = per_sm(152);
+  return s < blocks ? s : blocks;
+}
+
 template <int FMT, int TN>
 cudaError_t launch_narrow(const ProductCall& c) {
   using C = NarrowCfg<FMT, TN>;
@@ -121,11 +134,7 @@ cudaError_t launch_narrow(const ProductCall& c) {
   const ProductParams p = params<FMT>(c);
   const int64_t n_tiles = (p.n + 127) / 128, m_tiles = (p.m + TN - 1) / TN;
   const int blocks = (p.row_bytes_used + 127) / 128;
-  static const int want = getenv("SPLIT") ? atoi(getenv("SPLIT")) : 0;
-  int64_t split = 304 / (n_tiles * m_tiles);
-  split = split > 8 ? 8 : split < 1 ? 1 : split;
-  if (want) split = want;
-  if (split > blocks) split = blocks;
+  const int64_t split = narrow_split(n_tiles * m_tiles, blocks);
   Attributes l(dim3((unsigned)(n_tiles * split), (unsigned)m_tiles, 1), C::THREADS, C::SMEM, (unsigned)split, c);
   return cudaLaunchKernelEx(&l.cfg, kern, p, map_a, map_w);
 }
@@ -160,27 +169,42 @@ cudaError_t launch_wide(const ProductCall& c) {
   return cudaLaunchKernelEx(&l.cfg, kern, p, walk, maps);
 }
 
-// The forms' time in units of 10 ns, for the choice between them.  Measured on
-// GB300 (mxfp4, 512..8192 tokens x 7168..16384 columns x 2048..8192): a pair
-// takes 1.1 us and 0.32 us for each 128-byte block of K for a tile of 256
-// columns, 2.5 us and 0.40 us for one of 384; 76 pairs work at once.
+// The forms' times in units of 10 ns, for the choice between them, from graph
+// replays on GB300 of 1..8192 tokens x 1024..16384 columns x 2048..8192 (all
+// formats, inputs in L2).  A pair of the wide form takes 1.1 us and 0.32 us
+// for each 128-byte block of K for a tile of 256 columns, 2.5 us and 0.40 us
+// for one of 384; 76 pairs work at once; 6 us for the launch, the first loads
+// and the last stores.  The narrow form's 128-token tiles take in 34 KB for
+// each block, about 10 TB/s in all, and 5.5 us for the rest:
+//   tokens x columns x K       narrow     wide 256   wide 384
+//   128 x 7168 x 7168 mxfp4    12.3 us    15.2 us        -
+//   300 x 2050 x 7200 mxfp8    14.5       24.9           -
+//   256 x 7168 x 7168 mxfp4    16.7       15.4           -
+//   512 x 7168 x 7168 mxfp4    21.1       16.0       19.1 us
+//   1024 x 7168 x 7168 mxfp4     -        26.4       19.9
+//   8192 x 7168 x 7168 mxfp4     -       129        114
+//   4096 x 16384 x 2048 nvfp4    -        55.2       61.6
 int64_t wide_cost(const ProductCall& c, int64_t blocks, int tile_columns) {
   const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + tile_columns - 1) / tile_columns);
   const int64_t waves = (tiles + 75) / 76;
-  return waves * (tile_columns == 256 ? 110 + 32 * blocks : 250 + 40 * blocks);
+  return 600 + waves * (tile_columns == 256 ? 110 + 32 * blocks : 250 + 40 * blocks);
+}
+int64_t narrow_cost(const ProductCall& c, int64_t blocks) {
+  const int64_t tiles = (c.a->rows + 127) / 128 * ((c.w->rows + 127) / 128);
+  return 550 + tiles * blocks * 34 / 100;
 }
 
 template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
-  static const int wide = getenv("WIDE") ? atoi(getenv("WIDE")) : 256;
+  // up to 64 tokens the narrow form's time is that of reading the weights
   if (c.a->rows <= 16) return launch_narrow<FMT, 16>(c);
   if (c.a->rows <= 32) return launch_narrow<FMT, 32>(c);
   if (c.a->rows <= 64) return launch_narrow<FMT, 64>(c);
-  if (c.a->rows <= wide) return launch_narrow<FMT, 128>(c);
   const int64_t blocks = (c.a->cols * mx_bits(FMT) / 8 + 127) / 128;
-  static const int hv = getenv("HV") ? atoi(getenv("HV")) : 0;
-  if (hv ? hv == 2 : wide_cost(c, blocks, 384) < wide_cost(c, blocks, 256)) return launch_wide<FMT, 2>(c);
-  return launch_wide<FMT, 1>(c);
+  const int64_t wide1 = wide_cost(c, blocks, 256), wide2 = wide_cost(c, blocks, 384);
+  if (c.a->rows <= 65535 * 128 && narrow_cost(c, blocks) < (wide1 < wide2 ? wide1 : wide2))
+    return launch_narrow<FMT, 128>(c);
+  return wide1 <= wide2 ? launch_wide<FMT, 1>(c) : launch_wide<FMT, 2>(c);
 }
 
 }  // namespace

@@ -281,8 +281,12 @@ struct ProductParams {
 // A CTA makes a part of the sums of 128 output columns (weight rows, the
 // instruction's M) for TN tokens (its N): the part of its range of K.  The
 // CTAs of a cluster share one tile and split K evenly; their parts meet in
-// shared memory and are added up in rank order.  TN < 128 only with a single token tile: a tile's token
-// scales then start at the first of their scale tile's columns.
+// shared memory (over the stages, which are done with) and every CTA adds up,
+// in rank order, a share of the quadruples of columns, read from its peers.
+// (Sent instead -- st.async or bulk copies to the adding CTA -- the parts took
+// longer from 32 tokens on: 64 tokens x 7168 x 7168 10.9 us against 8.8.)
+// TN < 128 only with a single token tile: a tile's token scales then start at
+// the first of their scale tile's columns.
 constexpr int kMaxSplit = 8;  // the portable cluster size
 
 template <int FMT, int TN>
@@ -293,16 +297,16 @@ struct NarrowCfg {
   static constexpr uint32_t SF_BYTES = F::ATOMS * 512;
   static constexpr uint32_t STAGE = W_BYTES + A_BYTES + 2 * SF_BYTES;
   // two CTAs an SM, each with as many stages as half of its shared memory
-  // (227 KB less 1 KB a CTA) and half of TMEM hold
+  // and half of TMEM hold
   static constexpr int STAGES = (112 * 1024 - 1024) / STAGE;
   // TMEM columns: the accumulator, then for each stage its scales (so that a
   // stage's scales are replaced only after the products that read them)
   static constexpr int SF_COLS = F::ATOMS * 4;
   static constexpr int COLS_USED = TN + STAGES * 2 * SF_COLS;
   static constexpr int COLS = pow2_at_least(COLS_USED < 32 ? 32 : COLS_USED);
-  static_assert(STAGES >= 2 && COLS <= 256, "two CTAs an SM");
-  static constexpr uint32_t PARTS = TN * 128 * 4;  // fp32 sums of the tile, over the stages
-  static constexpr uint32_t SMEM = (STAGES * STAGE > PARTS ? STAGES * STAGE : PARTS) + 1024;
+  static_assert(STAGES >= 3 && COLS <= 256, "two CTAs an SM");
+  static_assert(STAGES * STAGE >= TN * 128 * 4, "the parts fit over the stages");
+  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
   static constexpr int THREADS = 192;
 };
 
@@ -321,50 +325,50 @@ __global__ void __launch_bounds__(192)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * S, done = empty + 8 * S;
   const uint32_t w_at = base, a_at = base + S * C::W_BYTES, sf_at = base + S * (C::W_BYTES + C::A_BYTES);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
-    fence_mbar_init();
-  }
-  if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), C::COLS);
-  tmem_fence_before();
-  __syncthreads();
-  tmem_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
   const int n0 = (int)(blockIdx.x / split) * 128, m0 = (int)blockIdx.y * TN;
   const int all_blocks = (p.row_bytes_used + 127) / 128;
   const int kb0 = (int)((int64_t)all_blocks * rank / split);
   const int blocks = (int)((int64_t)all_blocks * (rank + 1) / split) - kb0;
   bool failed = false;
-  // the output may still be in use by the preceding kernel; the loading thread
-  // waits later
-  if (threadIdx.x != 0) grid_dep_wait();
 
-  if (warp == 0 && lane == 0) {
-    const uint8_t* wsf = p.w_scales + (int64_t)(n0 / 128) * p.group_tiles * 512;
-    const uint8_t* asf = p.a_scales + (int64_t)(m0 / 128) * p.group_tiles * 512;
+  const uint8_t* const wsf = p.w_scales + (int64_t)(n0 / 128) * p.group_tiles * 512;
+  const uint8_t* const asf = p.a_scales + (int64_t)(m0 / 128) * p.group_tiles * 512;
+  const int ahead = blocks < S ? blocks : S;
+  auto sf_bytes = [&](int kb) {
+    const int64_t left = p.group_tiles - (int64_t)kb * F::ATOMS;
+    return (uint32_t)(left < F::ATOMS ? left : F::ATOMS) * 512u;
+  };
+  auto load_w = [&](int i, int s) {
+    const int kb = kb0 + i;
+    const uint32_t bar = full + 8 * s, sf = sf_bytes(kb);
+    mbar_arrive_expect_tx(bar, C::W_BYTES + C::A_BYTES + 2 * sf);
+    tma_load_2d(w_at + s * C::W_BYTES, &map_w, kb * 128, n0, bar);
+    bulk_load(sf_at + s * 2 * C::SF_BYTES, wsf + (int64_t)kb * F::ATOMS * 512, sf, bar);
+  };
+  auto load_a = [&](int i, int s) {
+    const int kb = kb0 + i;
+    const uint32_t bar = full + 8 * s;
+    tma_load_2d(a_at + s * C::A_BYTES, &map_a, kb * 128, m0, bar);
+    bulk_load(sf_at + s * 2 * C::SF_BYTES + C::SF_BYTES, asf + (int64_t)kb * F::ATOMS * 512, sf_bytes(kb), bar);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
+    fence_mbar_init();
     // the weights do not depend on the preceding kernel: the first stages'
     // are on their way before the wait for it
-    const int ahead = blocks < S ? blocks : S;
-    auto sf_bytes = [&](int kb) {
-      const int64_t left = p.group_tiles - (int64_t)kb * F::ATOMS;
-      return (uint32_t)(left < F::ATOMS ? left : F::ATOMS) * 512u;
-    };
-    auto load_w = [&](int i, int s) {
-      const int kb = kb0 + i;
-      const uint32_t bar = full + 8 * s, sf = sf_bytes(kb);
-      mbar_arrive_expect_tx(bar, C::W_BYTES + C::A_BYTES + 2 * sf);
-      tma_load_2d(w_at + s * C::W_BYTES, &map_w, kb * 128, n0, bar);
-      bulk_load(sf_at + s * 2 * C::SF_BYTES, wsf + (int64_t)kb * F::ATOMS * 512, sf, bar);
-    };
-    auto load_a = [&](int i, int s) {
-      const int kb = kb0 + i;
-      const uint32_t bar = full + 8 * s;
-      tma_load_2d(a_at + s * C::A_BYTES, &map_a, kb * 128, m0, bar);
-      bulk_load(sf_at + s * 2 * C::SF_BYTES + C::SF_BYTES, asf + (int64_t)kb * F::ATOMS * 512, sf_bytes(kb), bar);
-    };
     for (int i = 0; i < ahead; ++i) load_w(i, i);
-    grid_dep_wait();
+  }
+  grid_dep_wait();
+  if (threadIdx.x == 0)
     for (int i = 0; i < ahead; ++i) load_a(i, i);
+  if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), C::COLS);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
+
+  if (warp == 0 && lane == 0) {
     int issued = ahead;
     for (int i = ahead; i < blocks; ++i) {
       const int s = i % S;
@@ -401,18 +405,17 @@ __global__ void __launch_bounds__(192)
     if (issuer) mma_commit<1>(done);
     __syncwarp();
   }
-  // Warps 2..5 read the accumulator: warp w the TMEM lanes 32 (w % 4) .., that
-  // is the weight rows n0 + those.
-  const int row = 32 * (warp % 4) + lane;
-  const bool reader = warp >= 2;
   const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
-  if (reader) {
+  if (warp >= 2) {
+    // warp w reads the TMEM lanes 32 (w % 4) .., that is the weight rows n0 + those
+    const int row = 32 * (warp % 4) + lane;
     phase_or_flag(done, 0, failed, p.err, kErrStageTimeout);
     failed = __any_sync(0xffffffffu, failed);
     tmem_fence_after();
     grid_dep_launch_dependents();
     for (int c = 0; c < TN; c += 16) {
       uint32_t r[16];
+      if (m0 + c >= p.m) break;  // no token there
       tmem_ld16(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + c, r);
       tmem_ld_wait(r);
 #pragma unroll
@@ -422,7 +425,6 @@ __global__ void __launch_bounds__(192)
           if (!failed && n0 + row < p.n && m < p.m)
             p.out[m * p.out_row + n0 + row] = (uint16_t)pack_bf16x2(__uint_as_float(r[j]) * scale, 0.f);
         } else {
-          // the stages are free: every product that read them is complete
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)((c + j) * 128 + row) * 4u), "r"(r[j])
                        : "memory");
         }
@@ -431,12 +433,9 @@ __global__ void __launch_bounds__(192)
     tmem_fence_before();
   }
   __syncwarp();
-  __syncthreads();
   if (split > 1) {
     cluster_sync();
-    // every rank's threads take quadruples of output columns of some tokens;
-    // the loads of all parts are in flight together, their order of addition
-    // is that of the ranks
+    // the loads of all parts are in flight together
     const int64_t left = p.m - m0;
     const int quads = (left < TN ? (int)left : TN) * 32;
     for (int i = rank * C::THREADS + (int)threadIdx.x; i < quads; i += split * C::THREADS) {
@@ -472,11 +471,16 @@ __global__ void __launch_bounds__(192)
       }
     }
     __syncwarp();
-    cluster_sync();  // no CTA ends while its part is being read
+    cluster_arrive_release();  // no CTA ends while its part is being read
   }
+  __syncthreads();
   if (warp == 1) {
     tmem_fence_after();
     tmem_free<1>(tmem, C::COLS);
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_wait_acquire();
   }
 }
 
