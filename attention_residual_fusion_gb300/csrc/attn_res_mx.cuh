@@ -50,13 +50,15 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) {
   return __uint_as_float(code == 0u ? 0x00400000u : code == 255u ? 0x7fffffffu : code << 23);
 }
 
-// The scale of a group from the bits of its amax: the code, and what the
-// elements are multiplied (MX: the exact reciprocal of a power of two) or
-// divided (NVFP4) by; 0 where they all become zero.
+// The scale of a group from the bits of its amax: the code, what turns the
+// elements into code values, and a mask that clears the codes of a group
+// without a usable scale (not finite, or a product of scales of 0).
 template <int FMT>
 struct GroupScale {
   uint32_t code;
-  float by;
+  float by;       // MX: times this power of two; NVFP4: divided by this
+  float inverse;  // NVFP4: 1 / by, correctly rounded
+  uint32_t keep;
 };
 
 template <int FMT>
@@ -65,27 +67,36 @@ __device__ __forceinline__ GroupScale<FMT> group_scale(uint32_t amax, float g, f
   GroupScale<FMT> s;
   const bool bad = amax >= 0x7f800000u;
   if constexpr (M::NV) {
-    const float t = __uint_as_float(amax) / g6;
-    s.code = bad ? 0x7fu : (uint32_t)__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
-    s.by = bad ? 0.f : e4m3_value(s.code) * g;
+    const uint32_t c = (uint32_t)__nv_cvt_float_to_fp8(__uint_as_float(amax) / g6, __NV_SATFINITE, __NV_E4M3);
+    s.code = bad ? 0x7fu : c;
+    s.by = e4m3_value(c) * g;
+    s.inverse = 1.f / s.by;
+    s.keep = !bad && s.by > 0.f ? 0xffffffffu : 0u;
   } else {
     // amax = m * 2^E with 1 <= m < 2: the smallest 2^e with amax <= TOP * 2^e
-    // has e = E - TOP_EXP, or one more where m is above TOP's mantissa
-    int c = (int)(amax >> 23) - M::TOP_EXP + ((amax & 0x7fffffu) > M::TOP_MANT ? 1 : 0);
-    c = c < 0 ? 0 : c;
+    // has e = E - TOP_EXP, or one more where m is above TOP's mantissa (the
+    // sum below then carries into the exponent)
+    const int c = max((int)((amax + (0x7fffffu - M::TOP_MANT)) >> 23) - M::TOP_EXP, 0);
     s.code = bad ? 255u : (uint32_t)c;
-    s.by = bad ? 0.f : __uint_as_float((uint32_t)(254 - c) << 23);
+    s.by = __uint_as_float((uint32_t)(254 - c) << 23);
+    s.inverse = 0.f;
+    s.keep = bad ? 0u : 0xffffffffu;
   }
   return s;
 }
 
-template <int FMT>
-__device__ __forceinline__ float scaled_element(float x, float by) {
-  if constexpr (Mx<FMT>::NV) {
-    return by > 0.f ? x / by : 0.f;
-  } else {
-    return x * by;
-  }
+// -(x / by) for a pair, correctly rounded: the product with the correctly
+// rounded reciprocal, corrected once by its exact remainder (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): 3 instructions a pair in place of two divisions.  Nothing
+// over- or underflows on the way that matters: the divisor is between 2^-96
+// and 2^96, and where x is so small that its remainder is lost, the quotient
+// is far below half the smallest code.  Negated, because so a zero keeps its
+// sign (0 - 0 is +0 only in the remainder).
+__device__ __forceinline__ f32x2 negated_quotient2(f32x2 x, float by, float inverse) {
+  const f32x2 r = f2_make(-inverse, -inverse);
+  const f32x2 q = f2_mul(x, r);
+  return f2_fma(f2_fma(q, f2_make(by, by), x), r, q);
 }
 
 // Codes of eight elements: 8 bytes (MXFP8) or 4 (e2m1, the even column low).
@@ -94,36 +105,47 @@ struct Codes {
   uint32_t w[Mx<FMT>::FP8 ? 2 : 1];
 };
 
+// x: four pairs of neighbouring elements.
 template <int FMT>
-__device__ __forceinline__ Codes<FMT> encode8(const float (&x)[8], float by) {
-  Codes<FMT> c;
-  // by == 0: a group without a usable scale has zero elements (x itself may be NaN)
-  if (by == 0.f) {
-    c.w[0] = 0u;
-    if constexpr (Mx<FMT>::FP8) c.w[1] = 0u;
-    return c;
-  }
-  if constexpr (Mx<FMT>::FP8) {
+__device__ __forceinline__ Codes<FMT> encode8(const f32x2 (&x)[4], const GroupScale<FMT>& s) {
+  using M = Mx<FMT>;
+  f32x2 v[4];
+  if constexpr (M::NV) {
+    if (s.by >= 0x1p-96f && s.by <= 0x1p96f) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w = 0;
+      for (int i = 0; i < 4; ++i) v[i] = negated_quotient2(x[i], s.by, s.inverse);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 v = make_float2(scaled_element<FMT>(x[4 * h + 2 * i], by),
-                                     scaled_element<FMT>(x[4 * h + 2 * i + 1], by));
-        w |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (16 * i);
-      }
-      c.w[h] = w;
+      for (int i = 0; i < 4; ++i) v[i] = f2_make(-(f2_lo(x[i]) / s.by), -(f2_hi(x[i]) / s.by));
     }
   } else {
-    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = make_float2(scaled_element<FMT>(x[2 * i], by),
-                                   scaled_element<FMT>(x[2 * i + 1], by));
-      w |= (uint32_t)__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest) << (8 * i);
-    }
-    c.w[0] = w;
+    for (int i = 0; i < 4; ++i) v[i] = f2_mul(x[i], f2_make(s.by, s.by));
+  }
+  Codes<FMT> c;
+  if constexpr (M::FP8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm("{\n\t.reg .b16 a, b;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+          "mov.b32 %0, {a, b};\n\t}"
+          : "=r"(c.w[h])
+          : "f"(f2_lo(v[2 * h])), "f"(f2_hi(v[2 * h])), "f"(f2_lo(v[2 * h + 1])), "f"(f2_hi(v[2 * h + 1])));
+    c.w[0] &= s.keep;
+    c.w[1] &= s.keep;
+  } else {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(c.w[0])
+        : "f"(f2_lo(v[0])), "f"(f2_hi(v[0])), "f"(f2_lo(v[1])), "f"(f2_hi(v[1])), "f"(f2_lo(v[2])),
+          "f"(f2_hi(v[2])), "f"(f2_lo(v[3])), "f"(f2_hi(v[3])));
+    if constexpr (M::NV) c.w[0] ^= 0x88888888u;  // the codes' signs
+    c.w[0] &= s.keep;
   }
   return c;
 }
@@ -143,12 +165,19 @@ __device__ __forceinline__ void decode8(const Codes<FMT>& c, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
+// The largest magnitudes of eight bf16 values each of two rows, as 16-bit
+// patterns (a's low), which order like the magnitudes too: two at a time.
+__device__ __forceinline__ uint32_t amax_pair(const uint4& a, const uint4& b) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  const uint32_t ma = __vmaxu2(__vmaxu2(a.x & kAbs, a.y & kAbs), __vmaxu2(a.z & kAbs, a.w & kAbs));
+  const uint32_t mb = __vmaxu2(__vmaxu2(b.x & kAbs, b.y & kAbs), __vmaxu2(b.z & kAbs, b.w & kAbs));
+  return __vmaxu2(__byte_perm(ma, mb, 0x5410), __byte_perm(ma, mb, 0x7632));
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max2(uint32_t v) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = bf_lo(vword(v, k));
-    x[2 * k + 1] = bf_hi(vword(v, k));
-  }
+  for (int o = 1; o < LANES; o <<= 1) v = __vmaxu2(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // The scale word of four neighbouring groups, in the first lane of every
@@ -159,6 +188,19 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t code) {
   code |= __shfl_down_sync(0xffffffffu, code, L) << 8;
   code |= __shfl_down_sync(0xffffffffu, code, 2 * L) << 16;
   return code;
+}
+// The same for four rows at once, whose codes are the bytes of `codes`: the
+// words of the rows, a 4 x 4 transpose of bytes over four lanes.
+template <int FMT>
+__device__ __forceinline__ uint4 scale_words(uint32_t codes) {
+  constexpr int L = Mx<FMT>::LANES;
+  const uint32_t b = __shfl_down_sync(0xffffffffu, codes, L);
+  const uint32_t lo = __byte_perm(codes, b, 0x5140);  // rows 0, 1 of two groups
+  const uint32_t hi = __byte_perm(codes, b, 0x7362);  // rows 2, 3
+  const uint32_t lo2 = __shfl_down_sync(0xffffffffu, lo, 2 * L);
+  const uint32_t hi2 = __shfl_down_sync(0xffffffffu, hi, 2 * L);
+  return make_uint4(__byte_perm(lo, lo2, 0x5410), __byte_perm(lo, lo2, 0x7632), __byte_perm(hi, hi2, 0x5410),
+                    __byte_perm(hi, hi2, 0x7632));
 }
 
 template <int FMT>

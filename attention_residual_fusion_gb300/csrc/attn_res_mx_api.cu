@@ -135,22 +135,44 @@ attn_res_status_t run_rows(Kern pick, const attn_res_bf16_t* x, int64_t x_row, c
   p.x_row = x_row;
   p.q = view(*q);
   const int64_t padded = p.q.group_tiles * 4 * mx_group(q->format);
-  p.col_chunks = (padded + kMxWarpCols - 1) / kMxWarpCols;
-  p.jobs = (q->rows + 127) / 128 * 32 * p.col_chunks;
-  const int64_t ctas = (p.jobs + kMxThreads / 32 - 1) / (kMxThreads / 32);
-  if (ctas > INT32_MAX) return ATTN_RES_EINVAL;
+  const int64_t chunks = (padded + kMxWarpCols - 1) / kMxWarpCols;
+  const int64_t jobs = (q->rows + 127) / 128 * 32 * chunks;
+  if (jobs > INT32_MAX) return ATTN_RES_EINVAL;  // beyond any device's memory
+  p.col_chunks = static_cast<uint32_t>(chunks);
+  p.jobs = static_cast<uint32_t>(jobs);
+  const int64_t ctas = (jobs + kMxThreads / 32 - 1) / (kMxThreads / 32);
   Launch l(ctas, kMxThreads, flags, stream);
   return launched(cudaLaunchKernelEx(&l.cfg, pick(q->format), p));
 }
 
-using NormKernel = void (*)(MxNormParams);
-template <int VPT>
-NormKernel norm_kernel(int format) {
+// The norm's launch for a row of `nv` vectors.
+struct NormShape {
+  void (*kernel)(MxNormParams);
+  int threads;
+};
+template <int VPT, int MAX_THREADS, int MIN_CTAS>
+NormShape norm_shape(int format, int64_t nv) {
+  NormShape s;
+  s.threads = static_cast<int>(((nv + VPT - 1) / VPT + 31) / 32 * 32);
   switch (format) {
-    case ATTN_RES_MXFP8: return attn_res_mx_norm_kernel<ATTN_RES_MXFP8, VPT>;
-    case ATTN_RES_MXFP4: return attn_res_mx_norm_kernel<ATTN_RES_MXFP4, VPT>;
-    default: return attn_res_mx_norm_kernel<ATTN_RES_NVFP4, VPT>;
+    case ATTN_RES_MXFP8: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP8, VPT, MAX_THREADS, MIN_CTAS>; break;
+    case ATTN_RES_MXFP4: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP4, VPT, MAX_THREADS, MIN_CTAS>; break;
+    default: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_NVFP4, VPT, MAX_THREADS, MIN_CTAS>; break;
   }
+  return s;
+}
+// Vectors per thread by the row's width, and for rows of 4097..8192 columns by
+// their number: with few, more threads a row (H = 7168, T = 1 / 256: 2.4 / 4.7
+// us with 2 vectors each against 2.8 / 4.9 with 4); with many, four CTAs an SM
+// of 4 vectors a thread keep the most bytes on their way (T = 8192: 64.8 us,
+// 94 % of the copy rate; 78.7 with 2 vectors, 80.4 with two larger CTAs).
+NormShape norm_shape(int format, int64_t nv, int64_t rows) {
+  if (nv <= 256) return norm_shape<1, 256, 1>(format, nv);
+  if (nv <= 512) return norm_shape<2, 256, 1>(format, nv);
+  if (nv <= 1024 && rows < 1024) return norm_shape<2, 512, 2>(format, nv);
+  if (nv <= 1024) return norm_shape<4, 256, 4>(format, nv);
+  if (nv <= 4096) return norm_shape<8, 512, 1>(format, nv);
+  return norm_shape<8, 1024, 1>(format, nv);
 }
 
 }  // namespace
@@ -224,15 +246,10 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
   p.q = view(*q);
   // vectors of the row, with the groups that fill its last scale tile
   const int64_t nv = p.q.group_tiles * 4 * mx_group(q->format) / 8;
-  const int vpt = nv <= 256 ? 1 : nv <= 512 ? 2 : nv <= 1024 ? 4 : 8;
-  const int threads = static_cast<int>(((nv + vpt - 1) / vpt + 31) / 32 * 32);
+  const NormShape shape = norm_shape(q->format, nv, T);
   const int64_t pad_rows = (T + 127) / 128 * 128 - T;
-  const NormKernel kern = vpt == 1   ? norm_kernel<1>(q->format)
-                          : vpt == 2 ? norm_kernel<2>(q->format)
-                          : vpt == 4 ? norm_kernel<4>(q->format)
-                                     : norm_kernel<8>(q->format);
-  Launch l(T + (pad_rows + kMxPadRows - 1) / kMxPadRows, threads, flags, stream);
-  return launched(cudaLaunchKernelEx(&l.cfg, kern, p));
+  Launch l(T + (pad_rows + kMxPadRows - 1) / kMxPadRows, shape.threads, flags, stream);
+  return launched(cudaLaunchKernelEx(&l.cfg, shape.kernel, p));
 }
 
 attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t* w,

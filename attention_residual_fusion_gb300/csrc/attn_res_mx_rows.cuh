@@ -24,24 +24,23 @@ struct MxRowsParams {
   uint16_t* out;      // dequantise: result
   int64_t x_row;
   MxView q;
-  int64_t col_chunks;  // ceil(padded cols / 256)
-  int64_t jobs;        // row tiles * 32 * col_chunks
+  uint32_t col_chunks;  // ceil(padded cols / 256)
+  uint32_t jobs;        // row tiles * 32 * col_chunks
 };
 
 template <int FMT>
 __global__ void __launch_bounds__(kMxThreads) attn_res_mx_quantize_kernel(const MxRowsParams p) {
   using M = Mx<FMT>;
   const int lane = threadIdx.x & 31;
-  const int64_t job = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t job = blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
   const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   const float g6 = 6.f * g;
   grid_dep_wait();
   if (job < p.jobs) {
-    const int64_t chunk = job % p.col_chunks;
-    const int64_t rest = job / p.col_chunks;
+    const uint32_t rest = job / p.col_chunks;
     const int r = (int)(rest & 31);
     const int64_t tile = rest >> 5;
-    const int64_t vec = chunk * 32 + lane;
+    const int64_t vec = (int64_t)(job - rest * p.col_chunks) * 32 + lane;
     const bool in_row = vec * 8 < p.q.cols;
     uint4 v[4];
     bool ok[4];
@@ -51,23 +50,26 @@ __global__ void __launch_bounds__(kMxThreads) attn_res_mx_quantize_kernel(const 
       ok[u] = in_row && row < p.q.rows;
       v[u] = ok[u] ? ld_row(p.x + row * p.x_row + vec * 8) : make_uint4(0, 0, 0, 0);
     }
-    uint32_t word[4];
+    uint32_t codes = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x[8];
-      widen8(v[u], x);
-      uint32_t am = 0;
+    for (int u = 0; u < 4; u += 2) {
+      const uint32_t am = group_max2<M::LANES>(amax_pair(v[u], v[u + 1]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) am = max(am, abs_bits(x[i]));
-      const GroupScale<FMT> s = group_scale<FMT>(group_max<M::LANES>(am), g, g6);
-      if (ok[u])
-        st_codes<FMT>(p.q.data + (tile * 128 + 32 * u + r) * p.q.row_bytes, vec, encode8<FMT>(x, s.by));
-      word[u] = scale_word<FMT>(ok[u] ? s.code : 0u);
+      for (int e = 0; e < 2; ++e) {
+        const GroupScale<FMT> s = group_scale<FMT>(e == 0 ? am << 16 : am & 0xffff0000u, g, g6);
+        f32x2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = bf2_widen(vword(v[u + e], i));
+        if (ok[u + e]) {
+          st_codes<FMT>(p.q.data + (tile * 128 + 32 * (u + e) + r) * p.q.row_bytes, vec, encode8<FMT>(x, s));
+          codes |= s.code << (8 * (u + e));
+        }
+      }
     }
+    const uint4 words = scale_words<FMT>(codes);
     const int64_t atom = vec / M::ATOM_LANES;
     if (lane % M::ATOM_LANES == 0 && atom < p.q.group_tiles)
-      *reinterpret_cast<uint4*>(p.q.scales + ((tile * p.q.group_tiles + atom) * 512 + r * 16)) =
-          make_uint4(word[0], word[1], word[2], word[3]);
+      *reinterpret_cast<uint4*>(p.q.scales + ((tile * p.q.group_tiles + atom) * 512 + r * 16)) = words;
   }
   grid_dep_launch_dependents();
 }
@@ -78,15 +80,14 @@ template <int FMT>
 __global__ void __launch_bounds__(kMxThreads) attn_res_mx_dequantize_kernel(const MxRowsParams p) {
   using M = Mx<FMT>;
   const int lane = threadIdx.x & 31;
-  const int64_t job = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t job = blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
   const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   grid_dep_wait();
   if (job < p.jobs) {
-    const int64_t chunk = job % p.col_chunks;
-    const int64_t rest = job / p.col_chunks;
+    const uint32_t rest = job / p.col_chunks;
     const int r = (int)(rest & 31);
     const int64_t tile = rest >> 5;
-    const int64_t vec = chunk * 32 + lane;
+    const int64_t vec = (int64_t)(job - rest * p.col_chunks) * 32 + lane;
     if (vec * 8 < p.q.cols) {
       const int64_t group = vec / M::LANES;
       const uint4 sc = *reinterpret_cast<const uint4*>(
@@ -135,8 +136,8 @@ struct MxNormParams {
   MxView q;
 };
 
-template <int FMT, int VPT>
-__global__ void __launch_bounds__(VPT == 8 ? kMxNormMaxThreads : 256)
+template <int FMT, int VPT, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
     attn_res_mx_norm_kernel(const MxNormParams p) {
   using M = Mx<FMT>;
   __shared__ float part[32];
@@ -155,11 +156,6 @@ __global__ void __launch_bounds__(VPT == 8 ? kMxNormMaxThreads : 256)
     return;
   }
   uint4 w[VPT], c[VPT];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int i = tid + v * blockDim.x;
-    w[v] = i < nv ? ld_weight(p.weight + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
-  }
   const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   const float g6 = 6.f * g;
   grid_dep_wait();
@@ -180,20 +176,28 @@ __global__ void __launch_bounds__(VPT == 8 ? kMxNormMaxThreads : 256)
     for (int v = 0; v < VPT; ++v) c[v] = add_bf16x8(c[v], d[v]);
   }
   grid_dep_launch_dependents();
-  float sq = 0.f;
+  // after the addend, whose registers they take
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    float x[8];
-    widen8(c[v], x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
+    const int i = tid + v * blockDim.x;
+    w[v] = i < nv ? ld_weight(p.weight + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
   }
-  sq = warp_sum(sq);
+  f32x2 sq2 = f2_make(0.f, 0.f);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x2 x = bf2_widen(vword(c[v], k));
+      sq2 = f2_fma(x, x, sq2);
+    }
+  }
+  const float sq = warp_sum(f2_lo(sq2) + f2_hi(sq2));
   if (lane == 0) part[warp] = sq;
   __syncthreads();
   const int warps = blockDim.x >> 5;
   const float tot = warp_sum(lane < warps ? part[lane] : 0.f);
   const float rstd = __frsqrt_rn(fmaf(tot, p.inv_h, p.eps));
+  const f32x2 r2 = f2_make(rstd, rstd);
   uint8_t* const qrow = p.q.data + t * p.q.row_bytes;
   uint8_t* const srow =
       p.q.scales + (t / 128) * p.q.group_tiles * 512 + (t % 32) * 16 + (t % 128) / 32 * 4;
@@ -201,24 +205,23 @@ __global__ void __launch_bounds__(VPT == 8 ? kMxNormMaxThreads : 256)
   for (int v = 0; v < VPT; ++v) {
     const int i = tid + v * blockDim.x;
     const bool in_row = i < nv;
-    float x[8], wf[8];
-    widen8(c[v], x);
-    widen8(w[v], wf);
+    f32x2 y[4];
     uint32_t am = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // c * w is exact in fp32 (two 8-bit significands), so y is rounded once;
-      // past the row's end the zeros stay zeros, whatever the row's statistics
-      x[k] = in_row ? x[k] * wf[k] * rstd : 0.f;
-      am = max(am, abs_bits(x[k]));
+    for (int k = 0; k < 4; ++k) {
+      // c * w is exact in fp32 (two 8-bit significands), so y is rounded once
+      y[k] = f2_mul(f2_mul(bf2_widen(vword(c[v], k)), bf2_widen(vword(w[v], k))), r2);
+      am = max(am, max(abs_bits(f2_lo(y[k])), abs_bits(f2_hi(y[k]))));
     }
+    // past the row's end nothing counts, whatever the row's statistics make of 0
+    if (!in_row) am = 0;
     const GroupScale<FMT> s = group_scale<FMT>(group_max<M::LANES>(am), g, g6);
     if (in_row) {
-      st_codes<FMT>(qrow, i, encode8<FMT>(x, s.by));
+      st_codes<FMT>(qrow, i, encode8<FMT>(y, s));
       if (p.norm_out)
         st_row(p.norm_out + t * p.norm_row + (int64_t)i * 8,
-               make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+               make_uint4(pack_bf16x2(f2_lo(y[0]), f2_hi(y[0])), pack_bf16x2(f2_lo(y[1]), f2_hi(y[1])),
+                          pack_bf16x2(f2_lo(y[2]), f2_hi(y[2])), pack_bf16x2(f2_lo(y[3]), f2_hi(y[3]))));
       if (p.delta) st_row(prow + (int64_t)i * 8, c[v]);
     }
     const uint32_t word = scale_word<FMT>(in_row ? s.code : 0u);

@@ -132,6 +132,27 @@ def test_quantize(fmt, rows, cols, pad):
         assert x.intact() and q.intact()
 
 
+@pytest.mark.parametrize("g", [1.0, 0.0123, 3.7e-5, 911.0, 1e-31, 1e-37, 1e-41, 1e33])
+def test_quantize_nvfp4_quotients(g):
+    """Elements and scales are the correctly rounded fp32 quotients' codes, for
+    tensor scales from the smallest to the largest (torch divides in IEEE)."""
+    x = (activations(256, 4096, 6).double() * min(2688 * g, 1e37) / 150).bfloat16()
+    gt = torch.tensor([g], device="cuda")
+    q = mx.quantize(x, "nvfp4", gt)
+    xg = x.float().view(256, 256, 16)
+    s = (xg.abs().amax(-1) / (6.0 * gt)).clamp(max=448.0).to(torch.float8_e4m3fn)
+    got = q.scales.view(torch.uint8).permute(0, 3, 2, 1, 4).reshape(256, 256)
+    assert torch.equal(got, s.view(torch.uint8))
+    d = s.float()[..., None] * gt
+    v = torch.where(d > 0, xg / d, torch.zeros_like(xg)).view(256, 4096)
+    a = v.abs().clamp(max=6.0).double()
+    step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
+    n = torch.round(a / step) * step
+    code = torch.where(n <= 2, 2 * n, torch.where(n <= 4, n + 2, 7.0)).to(torch.uint8)
+    code |= torch.signbit(v).to(torch.uint8) << 3
+    assert torch.equal(q.data, code[:, ::2] | (code[:, 1::2] << 4))
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_quantize_allocates(fmt):
     x = activations(70, 416, 3)
