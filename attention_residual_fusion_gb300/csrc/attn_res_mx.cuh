@@ -90,8 +90,9 @@ __device__ __forceinline__ GroupScale<FMT> group_scale(uint32_t amax, float g, f
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): 3 instructions a pair in place of two divisions.  Nothing
 // over- or underflows on the way that matters: the divisor is between 2^-96
-// and 2^96, and where x is so small that its remainder is lost, the quotient
-// is far below half the smallest code.  Negated, because so a zero keeps its
+// and 2^96, the quotient at most 7 (the group's scale is not saturated), and
+// where x is so small that its remainder is lost, the quotient is far below
+// half the smallest code.  Negated, because so a zero keeps its
 // sign (0 - 0 is +0 only in the remainder).
 __device__ __forceinline__ f32x2 negated_quotient2(f32x2 x, float by, float inverse) {
   const f32x2 r = f2_make(-inverse, -inverse);
@@ -111,7 +112,7 @@ __device__ __forceinline__ Codes<FMT> encode8(const f32x2 (&x)[4], const GroupSc
   using M = Mx<FMT>;
   f32x2 v[4];
   if constexpr (M::NV) {
-    if (s.by >= 0x1p-96f && s.by <= 0x1p96f) {
+    if (s.code < 0x7eu && s.by >= 0x1p-96f && s.by <= 0x1p96f) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = negated_quotient2(x[i], s.by, s.inverse);
     } else {

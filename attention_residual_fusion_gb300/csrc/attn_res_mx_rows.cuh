@@ -15,7 +15,9 @@ namespace attn_res_dev {
 // 128-row tile: those rows' scales of four groups are the 16 consecutive
 // bytes of one entry of a scale tile, so a lane stores them at once, and the
 // entries of rows and groups that do not exist come out as zeros by the same
-// stores.  Four 16-byte loads per lane are in flight.
+// stores.  Four 16-byte loads per lane are in flight, and six CTAs an SM: on
+// 8192 x 7168 28.2 us to mxfp8, 25.4 to mxfp4 (86 % of the copy rate), 34.4 to
+// nvfp4, whose quotients bound it (with 8 CTAs 30.6, 26.2 and 36.1: spills).
 constexpr int kMxThreads = 256;
 constexpr int kMxWarpCols = 256;
 
@@ -29,7 +31,7 @@ struct MxRowsParams {
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kMxThreads) attn_res_mx_quantize_kernel(const MxRowsParams p) {
+__global__ void __launch_bounds__(kMxThreads, 6) attn_res_mx_quantize_kernel(const MxRowsParams p) {
   using M = Mx<FMT>;
   const int lane = threadIdx.x & 31;
   const uint32_t job = blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);

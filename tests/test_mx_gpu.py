@@ -132,11 +132,14 @@ def test_quantize(fmt, rows, cols, pad):
         assert x.intact() and q.intact()
 
 
-@pytest.mark.parametrize("g", [1.0, 0.0123, 3.7e-5, 911.0, 1e-31, 1e-37, 1e-41, 1e33])
-def test_quantize_nvfp4_quotients(g):
+@pytest.mark.parametrize("g,top", [(1.0, 2688), (0.0123, 30), (3.7e-5, 0.1), (911.0, 2e6), (1e-31, 2.6e-28),
+                                   (1e-37, 1e-34), (1e-41, 1e-38), (1e33, 1e37), (1.0, 1e37), (1e-31, 1e37),
+                                   (1e-40, 3e38), (0.5, 1e-30), (1e30, 1.0)])
+def test_quantize_nvfp4_quotients(g, top):
     """Elements and scales are the correctly rounded fp32 quotients' codes, for
-    tensor scales from the smallest to the largest (torch divides in IEEE)."""
-    x = (activations(256, 4096, 6).double() * min(2688 * g, 1e37) / 150).bfloat16()
+    tensor scales from the smallest to the largest, fitting the values or not
+    (torch divides in IEEE)."""
+    x = (activations(256, 4096, 6).double() * top / 150).clamp(-3e38, 3e38).bfloat16()
     gt = torch.tensor([g], device="cuda")
     q = mx.quantize(x, "nvfp4", gt)
     xg = x.float().view(256, 256, 16)
