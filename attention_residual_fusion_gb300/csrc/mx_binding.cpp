@@ -1,0 +1,272 @@
+// mx_binding.cpp -- Python binding of the microscaled entry points
+// (attn_res_mx_* of include/attn_res.h): argument marshalling only, as the
+// ctypes binding's, compiled because a decode step's calls take the GPU two to
+// six microseconds each and interpreted marshalling with two allocations took
+// fourteen.  PyTorch provides the device memory, the streams and the tensors.
+#include <ATen/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <pybind11/stl.h>
+#include <torch/csrc/utils/pybind.h>
+
+#include <optional>
+#include <string>
+#include <tuple>
+
+#include "attn_res.h"
+
+namespace py = pybind11;
+
+namespace {
+
+using OptTensor = std::optional<at::Tensor>;
+
+[[noreturn]] void refuse(const std::string& why) { throw py::value_error(why); }
+
+int format_code(const std::string& f) {
+  if (f == "mxfp8") return ATTN_RES_MXFP8;
+  if (f == "mxfp4") return ATTN_RES_MXFP4;
+  if (f == "nvfp4") return ATTN_RES_NVFP4;
+  refuse("format must be one of mxfp8, mxfp4, nvfp4");
+}
+const char* format_name(int f) {
+  return f == ATTN_RES_MXFP8 ? "mxfp8" : f == ATTN_RES_MXFP4 ? "mxfp4" : "nvfp4";
+}
+at::ScalarType data_type(int f) { return f == ATTN_RES_MXFP8 ? at::kFloat8_e4m3fn : at::kByte; }
+at::ScalarType scales_type(int f) { return f == ATTN_RES_NVFP4 ? at::kFloat8_e4m3fn : at::kFloat8_e8m0fnu; }
+std::array<int64_t, 5> scales_shape(int f, int64_t rows, int64_t cols) {
+  return {(rows + 127) / 128, (cols / (f == ATTN_RES_NVFP4 ? 16 : 32) + 3) / 4, 32, 4, 4};
+}
+
+at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
+  return at::detail::empty_cuda(shape, type, device, std::nullopt);
+}
+
+// The stride of a single row says nothing (it may be anything): such a matrix
+// gets the least that the entry points take.
+int64_t row_stride(const at::Tensor& t, int64_t to) {
+  return t.size(0) > 1 ? t.stride(0) : (t.size(1) + to - 1) / to * to;
+}
+
+struct MxTensor {
+  at::Tensor data, scales;
+  OptTensor global_scale;
+  attn_res_mx_t c = {};
+
+  MxTensor(at::Tensor d, at::Tensor s, int f, OptTensor g, int64_t rows, int64_t cols)
+      : data(std::move(d)), scales(std::move(s)), global_scale(std::move(g)) {
+    c.format = f;
+    c.rows = rows;
+    c.cols = cols;
+    c.data = data.data_ptr();
+    c.row_bytes = row_stride(data, 16);
+    c.scales = static_cast<uint8_t*>(scales.data_ptr());
+    c.tensor_scale = global_scale ? static_cast<const float*>(global_scale->data_ptr()) : nullptr;
+  }
+  at::Device device() const { return data.device(); }
+};
+
+void check_global_scale(int f, const OptTensor& g, at::Device device) {
+  if (g && (f != ATTN_RES_NVFP4 || g->scalar_type() != at::kFloat || g->numel() != 1 || g->device() != device))
+    refuse("global_scale must be one float32 beside the data (nvfp4 only)");
+}
+
+MxTensor make(const at::Tensor& data, const at::Tensor& scales, const std::string& format, const OptTensor& g) {
+  const int f = format_code(format);
+  if (data.scalar_type() != data_type(f) || data.dim() != 2 || !data.is_cuda() ||
+      (data.stride(1) != 1 && data.size(1) > 1))
+    refuse(std::string("data must be a CUDA ") + c10::toString(data_type(f)) + " matrix with unit inner stride");
+  const int64_t rows = data.size(0), cols = data.size(1) * (f == ATTN_RES_MXFP8 ? 1 : 2);
+  const auto shape = scales_shape(f, rows, cols);
+  if (scales.scalar_type() != scales_type(f) || scales.device() != data.device() ||
+      scales.sizes() != at::IntArrayRef(shape) || !scales.is_contiguous())
+    refuse(std::string("scales must be a contiguous ") + c10::toString(scales_type(f)) +
+           " tensor of scales_shape(format, rows, cols) beside data");
+  check_global_scale(f, g, data.device());
+  return MxTensor(data, scales, f, g, rows, cols);
+}
+
+void check_shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0 || cols % 32) refuse("rows must be >= 0 and the width a positive multiple of 32");
+}
+
+MxTensor allocate(int64_t rows, int64_t cols, int f, const OptTensor& g, at::Device device) {
+  check_shape(rows, cols);
+  check_global_scale(f, g, device);
+  return MxTensor(new_tensor({rows, f == ATTN_RES_MXFP8 ? cols : cols / 2}, data_type(f), device),
+                  new_tensor(scales_shape(f, rows, cols), scales_type(f), device), f, g, rows, cols);
+}
+
+void check_rows(const char* name, const at::Tensor& t) {
+  if (t.scalar_type() != at::kBFloat16 || !t.is_cuda()) refuse(std::string(name) + " must be a CUDA bfloat16 tensor");
+  if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
+    refuse(std::string(name) + " must be a 2-D matrix with unit inner stride");
+}
+void check_rows(const char* name, const at::Tensor& t, int64_t rows, int64_t cols, at::Device device) {
+  check_rows(name, t);
+  if (t.size(0) != rows || t.size(1) != cols)
+    refuse(std::string(name) + " must be a [" + std::to_string(rows) + ", " + std::to_string(cols) + "] matrix");
+  if (t.device() != device) refuse("all tensors of a call must be on one device");
+}
+attn_res_bf16_t* bf16(const at::Tensor& t) { return static_cast<attn_res_bf16_t*>(t.data_ptr()); }
+
+// The device and stream of a call: current while outputs are allocated and the
+// kernel is launched.
+struct On {
+  c10::cuda::OptionalCUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard stream;
+  void* handle;
+  On(at::Device d, const py::object& s) {
+    if (s.is_none()) {
+      device.set_device(d);
+      handle = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+    } else {
+      const auto given = c10::cuda::CUDAStream::unpack3(
+          s.attr("stream_id").cast<int64_t>(), static_cast<c10::DeviceIndex>(s.attr("device_index").cast<int64_t>()),
+          static_cast<c10::DeviceType>(s.attr("device_type").cast<int64_t>()));
+      if (given.device() != d) refuse("stream must belong to the tensors' device");
+      stream.reset_stream(given);
+      handle = given.stream();
+    }
+  }
+};
+
+void check(attn_res_status_t st) {
+  if (st == ATTN_RES_OK) return;
+  const py::object type = py::module_::import("attention_residual_fusion_gb300").attr("AttnResError");
+  const py::object error = type(static_cast<int>(st), attn_res_status_string(st));
+  PyErr_SetObject(type.ptr(), error.ptr());
+  throw py::error_already_set();
+}
+uint32_t flags_of(bool pdl) { return pdl ? ATTN_RES_FLAG_PDL : 0u; }
+
+// The result of a quantising call: `out`, checked, or a new one.
+py::object result(const py::object& out, int64_t rows, int64_t cols, const std::string& format, const OptTensor& g,
+                  at::Device device, const attn_res_mx_t** c) {
+  const int f = format_code(format);
+  if (out.is_none()) {
+    py::object made = py::cast(allocate(rows, cols, f, g, device));
+    *c = &made.cast<MxTensor&>().c;
+    return made;
+  }
+  const MxTensor& o = out.cast<const MxTensor&>();
+  if (o.c.format != f || (g && !(o.global_scale && g->is_same(*o.global_scale))))
+    refuse("out has another format or global_scale");
+  if (o.c.rows != rows || o.c.cols != cols || o.device() != device)
+    refuse("out must be an MxTensor of the rows' shape, on their device");
+  *c = &o.c;
+  return out;
+}
+
+py::object quantize(const at::Tensor& x, const std::string& format, const OptTensor& global_scale,
+                    const py::object& out, bool pdl, const py::object& stream) {
+  check_rows("x", x);
+  const On on(x.device(), stream);
+  const attn_res_mx_t* c;
+  py::object q = result(out, x.size(0), x.size(1), format, global_scale, x.device(), &c);
+  check(attn_res_mx_quantize(bf16(x), row_stride(x, 8), c, flags_of(pdl), on.handle));
+  return q;
+}
+
+at::Tensor dequantize(const MxTensor& q, const OptTensor& out, bool pdl, const py::object& stream) {
+  const On on(q.device(), stream);
+  if (out) check_rows("out", *out, q.c.rows, q.c.cols, q.device());
+  at::Tensor x = out ? *out : new_tensor({q.c.rows, q.c.cols}, at::kBFloat16, q.device());
+  check(attn_res_mx_dequantize(&q.c, bf16(x), row_stride(x, 8), flags_of(pdl), on.handle));
+  return x;
+}
+
+py::object add_rms_norm(const at::Tensor& prefix, const OptTensor& delta, const at::Tensor& weight, double eps,
+                        const std::string& format, const OptTensor& global_scale, const py::object& out,
+                        const OptTensor& norm_out, bool pdl, const py::object& stream) {
+  check_rows("prefix", prefix);
+  const at::Device device = prefix.device();
+  const int64_t rows = prefix.size(0), cols = prefix.size(1);
+  if (delta) check_rows("delta", *delta, rows, cols, device);
+  if (norm_out) check_rows("norm_out", *norm_out, rows, cols, device);
+  if (weight.scalar_type() != at::kBFloat16 || weight.device() != device || weight.dim() != 1 ||
+      weight.size(0) != cols || !weight.is_contiguous())
+    refuse("weight must be a contiguous bfloat16 [H] tensor beside prefix");
+  const On on(device, stream);
+  const attn_res_mx_t* c;
+  py::object q = result(out, rows, cols, format, global_scale, device, &c);
+  check(attn_res_mx_norm(bf16(prefix), row_stride(prefix, 8), delta ? bf16(*delta) : nullptr,
+                         delta ? row_stride(*delta, 8) : 0, bf16(weight), static_cast<float>(eps),
+                         norm_out ? bf16(*norm_out) : nullptr, norm_out ? row_stride(*norm_out, 8) : 0, c,
+                         flags_of(pdl), on.handle));
+  return q;
+}
+
+at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bool pdl, const py::object& stream) {
+  const at::Device device = a.device();
+  const int64_t m = a.c.rows, n = w.c.rows;
+  if (a.c.format != w.c.format || a.c.cols != w.c.cols) refuse("a and w must have one format and one width");
+  if (w.device() != device) refuse("all tensors of a call must be on one device");
+  const On on(device, stream);
+  at::Tensor y;
+  int64_t row;
+  if (out) {
+    check_rows("out", *out, m, n, device);
+    y = *out;
+    row = row_stride(y, 8);
+  } else {
+    row = (n + 7) / 8 * 8;  // rows start on 16-byte boundaries, whatever n
+    y = new_tensor({m, row}, at::kBFloat16, device);
+    if (row != n) y = y.narrow(1, 0, n);
+  }
+  check(attn_res_mx_matmul(&a.c, &w.c, bf16(y), row, flags_of(pdl), on.handle));
+  return y;
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_mx, m) {
+  using namespace py::literals;
+  py::class_<MxTensor>(m, "MxTensor", R"(A matrix [rows, cols] in a microscaled format.
+
+data: [rows, cols] float8_e4m3fn ("mxfp8") or [rows, cols // 2] uint8 (two
+e2m1 codes a byte, the even column low), unit inner stride; scales:
+``scales_shape(format, rows, cols)``, contiguous, float8_e8m0fnu or (nvfp4)
+float8_e4m3fn; global_scale: one fp32 on the device, nvfp4 only, or None.)")
+      .def(py::init(&make), "data"_a, "scales"_a, "format"_a, "global_scale"_a = py::none())
+      .def_static(
+          "empty",
+          [](int64_t rows, int64_t cols, const std::string& format, const OptTensor& g, const py::object& device) {
+            const int f = format_code(format);
+            check_shape(rows, cols);
+            at::Device d = py::module_::import("torch").attr("device")(device).cast<at::Device>();
+            if (!d.is_cuda()) refuse("the device must be a CUDA device");
+            if (!d.has_index()) d = at::Device(at::kCUDA, c10::cuda::current_device());
+            return allocate(rows, cols, f, g, d);
+          },
+          "rows"_a, "cols"_a, "format"_a, "global_scale"_a = py::none(), "device"_a = "cuda",
+          "Uninitialised codes and scales for [rows, cols] (cols a multiple of 32).")
+      .def_property_readonly("data", [](const MxTensor& t) { return t.data; })
+      .def_property_readonly("scales", [](const MxTensor& t) { return t.scales; })
+      .def_property_readonly("global_scale", [](const MxTensor& t) { return t.global_scale; })
+      .def_property_readonly("format", [](const MxTensor& t) { return format_name(t.c.format); })
+      .def_property_readonly("shape", [](const MxTensor& t) { return std::make_tuple(t.c.rows, t.c.cols); })
+      .def_property_readonly("device", [](const MxTensor& t) { return t.device(); });
+  m.def("quantize", &quantize, "x"_a, "format"_a = "mxfp4", "global_scale"_a = py::none(), "out"_a = py::none(),
+        py::kw_only(), "pdl"_a = false, "stream"_a = py::none(),
+        R"(bf16 rows [rows, cols] to ``format`` (attn_res_mx_quantize).  cols is a
+multiple of 32; ``global_scale`` (nvfp4) is the tensor's scale, 1 if None.
+Returns ``out`` (allocated if not given; its own global_scale then holds).)");
+  m.def("dequantize", &dequantize, "q"_a, "out"_a = py::none(), py::kw_only(), "pdl"_a = false,
+        "stream"_a = py::none(),
+        "The bf16 values [rows, cols] that ``q`` stands for (attn_res_mx_dequantize).");
+  m.def("add_rms_norm", &add_rms_norm, "prefix"_a, "delta"_a.none(true), "weight"_a, "eps"_a = 1e-6,
+        "format"_a = "mxfp8", "global_scale"_a = py::none(), "out"_a = py::none(), "norm_out"_a = py::none(),
+        py::kw_only(), "pdl"_a = false, "stream"_a = py::none(),
+        R"(Residual addition and RMSNorm of token rows, quantised (attn_res_mx_norm).
+
+c = bf16(prefix + delta) (prefix if ``delta`` is None; prefix [T, H] is
+updated in place otherwise), y = c * weight / sqrt(mean(c^2) + eps); the
+result is y in ``format``, from fp32.  ``norm_out`` [T, H] receives y in
+bf16 as well, if given.  H is a multiple of 32, at most 65536.)");
+  m.def("matmul", &matmul, "a"_a, "w"_a, "out"_a = py::none(), py::kw_only(), "pdl"_a = false,
+        "stream"_a = py::none(),
+        R"(``a`` [m, k] times the transpose of ``w`` [n, k], of one format: bf16
+[m, n], fp32 sums (attn_res_mx_matmul).)");
+}

@@ -196,7 +196,7 @@ def test_null_matrices(lib):
     assert ar.lib().attn_res_mx_matmul(matrix(1), null, addr(0), 72, 0, None) == 1
 
 
-def test_binding_refuses_what_is_not_on_the_gpu():
+def test_binding_refuses_what_is_not_on_the_gpu(lib):
     with pytest.raises(ValueError):
         mx.quantize(torch.zeros(4, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
