@@ -255,8 +255,10 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
 attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t* w,
                                      attn_res_bf16_t* out, int64_t out_row, uint32_t flags,
                                      void* stream) {
+  const int kernel = static_cast<int>((flags >> 16) & 0xfu), split = static_cast<int>((flags >> 8) & 0xffu);
   if (!scalars_ok(a) || !scalars_ok(w) || a->format != w->format || a->cols != w->cols ||
-      !known_flags(flags))
+      !known_flags(flags & ~(ATTN_RES_FLAG_KERNEL(0xf) | ATTN_RES_FLAG_SPLIT(0xff))) ||
+      !product_overrides_ok(*a, kernel, split))
     return ATTN_RES_EINVAL;
   if (a->rows == 0 || w->rows == 0) return ATTN_RES_OK;
   attn_res_status_t st = check_matrix(*a);
@@ -281,6 +283,8 @@ attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t
   c.out = out;
   c.out_row = out_row;
   c.pdl = (flags & ATTN_RES_FLAG_PDL) != 0;
+  c.kernel = kernel;
+  c.split = split;
   c.stream = static_cast<cudaStream_t>(stream);
   return launched(launch_mx_product(c));
 }

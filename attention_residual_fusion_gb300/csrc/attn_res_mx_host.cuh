@@ -20,10 +20,14 @@ struct ProductCall {
   attn_res_bf16_t* out;
   int64_t out_row;
   bool pdl;
+  int kernel;  // ATTN_RES_MX_*, 0 automatic
+  int split;   // of the narrow form, 0 automatic
   int device;
   unsigned* err;
   cudaStream_t stream;
 };
 cudaError_t launch_mx_product(const ProductCall& c);
+// Whether the overrides can be met.
+bool product_overrides_ok(const attn_res_mx_t& a, int kernel, int split);
 
 }  // namespace attn_res_host

@@ -114,7 +114,7 @@ struct Attributes {
 int64_t narrow_split(int64_t tiles, int64_t blocks) {
   auto per_sm = [&](int64_t ctas) {
     const int64_t s = ctas / tiles;
-    return s > 6 ? 6 : s < 1 ? 1 : s;
+    return s > kMaxSplit ? kMaxSplit : s < 1 ? 1 : s;
   };
   int64_t s = per_sm(304);
   if (s * tiles < 228) s = per_sm(152);
@@ -134,7 +134,7 @@ cudaError_t launch_narrow(const ProductCall& c) {
   const ProductParams p = params<FMT>(c);
   const int64_t n_tiles = (p.n + 127) / 128, m_tiles = (p.m + TN - 1) / TN;
   const int blocks = (p.row_bytes_used + 127) / 128;
-  const int64_t split = narrow_split(n_tiles * m_tiles, blocks);
+  const int64_t split = c.split ? c.split : narrow_split(n_tiles * m_tiles, blocks);
   Attributes l(dim3((unsigned)(n_tiles * split), (unsigned)m_tiles, 1), C::THREADS, C::SMEM, (unsigned)split, c);
   return cudaLaunchKernelEx(&l.cfg, kern, p, map_a, map_w);
 }
@@ -194,17 +194,28 @@ int64_t narrow_cost(const ProductCall& c, int64_t blocks) {
   return 550 + tiles * blocks * 34 / 100;
 }
 
+// Token tiles of the narrow form's grid (its y).
+constexpr int64_t kNarrowMaxRows = int64_t(65535) * 128;
+int64_t k_blocks(const attn_res_mx_t& a) { return (a.cols * mx_bits(a.format) / 8 + 127) / 128; }
+
 template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
-  // up to 64 tokens the narrow form's time is that of reading the weights
-  if (c.a->rows <= 16) return launch_narrow<FMT, 16>(c);
-  if (c.a->rows <= 32) return launch_narrow<FMT, 32>(c);
-  if (c.a->rows <= 64) return launch_narrow<FMT, 64>(c);
-  const int64_t blocks = (c.a->cols * mx_bits(FMT) / 8 + 127) / 128;
-  const int64_t wide1 = wide_cost(c, blocks, 256), wide2 = wide_cost(c, blocks, 384);
-  if (c.a->rows <= 65535 * 128 && narrow_cost(c, blocks) < (wide1 < wide2 ? wide1 : wide2))
-    return launch_narrow<FMT, 128>(c);
-  return wide1 <= wide2 ? launch_wide<FMT, 1>(c) : launch_wide<FMT, 2>(c);
+  const int64_t rows = c.a->rows, blocks = k_blocks(*c.a);
+  int kernel = c.kernel;
+  if (kernel == 0) {
+    const int64_t one = wide_cost(c, blocks, 256), two = wide_cost(c, blocks, 384);
+    // up to 64 tokens the narrow form's time is that of reading the weights
+    if (rows <= 64 || (rows <= kNarrowMaxRows && narrow_cost(c, blocks) < (one < two ? one : two)))
+      kernel = ATTN_RES_MX_NARROW;
+    else
+      kernel = one <= two ? ATTN_RES_MX_WIDE : ATTN_RES_MX_WIDER;
+  }
+  if (kernel == ATTN_RES_MX_WIDE) return launch_wide<FMT, 1>(c);
+  if (kernel == ATTN_RES_MX_WIDER) return launch_wide<FMT, 2>(c);
+  if (rows <= 16) return launch_narrow<FMT, 16>(c);
+  if (rows <= 32) return launch_narrow<FMT, 32>(c);
+  if (rows <= 64) return launch_narrow<FMT, 64>(c);
+  return launch_narrow<FMT, 128>(c);
 }
 
 }  // namespace
@@ -216,6 +227,12 @@ cudaError_t launch_mx_product(const ProductCall& c) {
     case ATTN_RES_NVFP4: return launch_format<ATTN_RES_NVFP4>(c);
     default: return cudaErrorInvalidValue;
   }
+}
+
+bool product_overrides_ok(const attn_res_mx_t& a, int kernel, int split) {
+  if (kernel < 0 || kernel > ATTN_RES_MX_WIDER) return false;
+  if (kernel == ATTN_RES_MX_NARROW) return a.rows <= kNarrowMaxRows && split <= kMaxSplit && split <= k_blocks(a);
+  return split == 0;
 }
 
 }  // namespace attn_res_host

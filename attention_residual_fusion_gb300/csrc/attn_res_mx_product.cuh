@@ -282,12 +282,13 @@ struct ProductParams {
 // instruction's M) for TN tokens (its N): the part of its range of K.  The
 // CTAs of a cluster share one tile and split K evenly; their parts meet in
 // shared memory (over the stages, which are done with) and every CTA adds up,
-// in rank order, a share of the quadruples of columns, read from its peers.
+// in an order fixed by the tile, a share of the sums, read from its peers.
 // (Sent instead -- st.async or bulk copies to the adding CTA -- the parts took
 // longer from 32 tokens on: 64 tokens x 7168 x 7168 10.9 us against 8.8.)
 // TN < 128 only with a single token tile: a tile's token scales then start at
 // the first of their scale tile's columns.
-constexpr int kMaxSplit = 8;  // the portable cluster size
+constexpr int kMaxSplit = 6;
+constexpr int kItems = 4;  // of the joining, per thread and pass
 
 template <int FMT, int TN>
 struct NarrowCfg {
@@ -310,8 +311,21 @@ struct NarrowCfg {
   static constexpr int THREADS = 192;
 };
 
+// One output column of four tokens, as far as they exist.
+__device__ __forceinline__ void store_quad(const ProductParams& p, int64_t m, int64_t n, float a, float b, float c,
+                                           float d, bool failed) {
+  if (n >= p.n) return;
+  const uint32_t lo = pack_bf16x2(a, b), hi = pack_bf16x2(c, d);
+  if (failed) return;
+  uint16_t* const o = p.out + m * p.out_row + n;
+  if (m < p.m) o[0] = (uint16_t)lo;
+  if (m + 1 < p.m) o[p.out_row] = (uint16_t)(lo >> 16);
+  if (m + 2 < p.m) o[2 * p.out_row] = (uint16_t)hi;
+  if (m + 3 < p.m) o[3 * p.out_row] = (uint16_t)(hi >> 16);
+}
+
 template <int FMT, int TN>
-__global__ void __launch_bounds__(192)
+__global__ void __launch_bounds__(192, 2)
     attn_res_mx_product_narrow_kernel(const ProductParams p, const __grid_constant__ CUtensorMap map_a,
                                       const __grid_constant__ CUtensorMap map_w) {
   using C = NarrowCfg<FMT, TN>;
@@ -413,19 +427,22 @@ __global__ void __launch_bounds__(192)
     failed = __any_sync(0xffffffffu, failed);
     tmem_fence_after();
     grid_dep_launch_dependents();
-    for (int c = 0; c < TN; c += 16) {
-      uint32_t r[16];
+    constexpr int CH = TN >= 64 ? 64 : 16;  // tokens at a time
+    for (int c = 0; c < TN; c += CH) {
       if (m0 + c >= p.m) break;  // no token there
-      tmem_ld16(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + c, r);
+      uint32_t r[CH];
+      const uint32_t at = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + c;
+      if constexpr (CH == 64) tmem_ld64(at, r);
+      else tmem_ld16(at, r);
       tmem_ld_wait(r);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < CH; j += 4) {
         if (split == 1) {
-          const int64_t m = m0 + c + j;
-          if (!failed && n0 + row < p.n && m < p.m)
-            p.out[m * p.out_row + n0 + row] = (uint16_t)pack_bf16x2(__uint_as_float(r[j]) * scale, 0.f);
+          store_quad(p, m0 + c + j, n0 + row, __uint_as_float(r[j]) * scale, __uint_as_float(r[j + 1]) * scale,
+                     __uint_as_float(r[j + 2]) * scale, __uint_as_float(r[j + 3]) * scale, failed);
         } else {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)((c + j) * 128 + row) * 4u), "r"(r[j])
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c + j) * 32 + row) * 16u),
+                       "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
                        : "memory");
         }
       }
@@ -435,43 +452,52 @@ __global__ void __launch_bounds__(192)
   __syncwarp();
   if (split > 1) {
     cluster_sync();
-    // the loads of all parts are in flight together
+    // a thread's items are quadruples of tokens of one column; the loads of all
+    // parts of kItems of them are in flight together
     const int64_t left = p.m - m0;
-    const int quads = (left < TN ? (int)left : TN) * 32;
-    for (int i = rank * C::THREADS + (int)threadIdx.x; i < quads; i += split * C::THREADS) {
-      const uint32_t at = base + (uint32_t)i * 16u;
-      float4 part[kMaxSplit];
+    const int items = ((left < TN ? (int)left : TN) + 3) / 4 * 128;
+    const int stride = split * C::THREADS;
+    for (int i0 = rank * C::THREADS + (int)threadIdx.x; i0 < items; i0 += kItems * stride) {
+      float4 part[kItems][kMaxSplit];  // [.][k]: of rank (rank + k) % split, the own one from here
 #pragma unroll
-      for (int r = 0; r < kMaxSplit; ++r)
-        if (r < split)
-          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                       : "=f"(part[r].x), "=f"(part[r].y), "=f"(part[r].z), "=f"(part[r].w)
-                       : "r"(map_rank(at, (uint32_t)r))
-                       : "memory");
-      float4 sum = part[0];
+      for (int k = 0; k < kItems; ++k) {
+        const int i = i0 + k * stride;
+        const uint32_t at = base + (uint32_t)i * 16u;
+        if (i >= items || n0 + i % 128 >= p.n) continue;
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(part[k][0].x), "=f"(part[k][0].y), "=f"(part[k][0].z), "=f"(part[k][0].w)
+                     : "r"(at)
+                     : "memory");
 #pragma unroll
-      for (int r = 1; r < kMaxSplit; ++r)
-        if (r < split) {
-          sum.x += part[r].x;
-          sum.y += part[r].y;
-          sum.z += part[r].z;
-          sum.w += part[r].w;
-        }
-      const int n = n0 + i % 32 * 4;
-      uint16_t* const o = p.out + (m0 + i / 32) * p.out_row + n;
-      const uint2 v = make_uint2(pack_bf16x2(sum.x * scale, sum.y * scale),
-                                 pack_bf16x2(sum.z * scale, sum.w * scale));
-      if (failed) continue;
-      if (n + 4 <= p.n) {
-        *reinterpret_cast<uint2*>(o) = v;
-      } else {
-        if (n < p.n) o[0] = (uint16_t)v.x;
-        if (n + 1 < p.n) o[1] = (uint16_t)(v.x >> 16);
-        if (n + 2 < p.n) o[2] = (uint16_t)v.y;
+        for (int r = 1; r < kMaxSplit; ++r)
+          if (r < split)
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(part[k][r].x), "=f"(part[k][r].y), "=f"(part[k][r].z), "=f"(part[k][r].w)
+                         : "r"(map_rank(at, (uint32_t)(rank + r < split ? rank + r : rank + r - split)))
+                         : "memory");
+      }
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int i = i0 + k * stride;
+        if (i >= items || n0 + i % 128 >= p.n) continue;
+        float4 sum = part[k][0];
+#pragma unroll
+        for (int r = 1; r < kMaxSplit; ++r)
+          if (r < split) {
+            sum.x += part[k][r].x;
+            sum.y += part[k][r].y;
+            sum.z += part[k][r].z;
+            sum.w += part[k][r].w;
+          }
+        store_quad(p, m0 + i / 128 * 4, n0 + i % 128, sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale,
+                   failed);
       }
     }
+    // No CTA ends while its part is being read.  Every load's value has been
+    // used by then, so the arrival orders nothing (releasing the results'
+    // stores with it took some 2000 clocks more).
     __syncwarp();
-    cluster_arrive_release();  // no CTA ends while its part is being read
+    cluster_arrive_relaxed();
   }
   __syncthreads();
   if (warp == 1) {

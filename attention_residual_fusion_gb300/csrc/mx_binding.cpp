@@ -198,7 +198,8 @@ py::object add_rms_norm(const at::Tensor& prefix, const OptTensor& delta, const 
   return q;
 }
 
-at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bool pdl, const py::object& stream) {
+at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bool pdl, int kernel, int split,
+                  const py::object& stream) {
   const at::Device device = a.device();
   const int64_t m = a.c.rows, n = w.c.rows;
   if (a.c.format != w.c.format || a.c.cols != w.c.cols) refuse("a and w must have one format and one width");
@@ -215,7 +216,9 @@ at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bo
     y = new_tensor({m, row}, at::kBFloat16, device);
     if (row != n) y = y.narrow(1, 0, n);
   }
-  check(attn_res_mx_matmul(&a.c, &w.c, bf16(y), row, flags_of(pdl), on.handle));
+  if (kernel < 0 || kernel > 15 || split < 0 || split > 255) refuse("no such kernel or split");
+  check(attn_res_mx_matmul(&a.c, &w.c, bf16(y), row,
+                           flags_of(pdl) | ATTN_RES_FLAG_KERNEL(kernel) | ATTN_RES_FLAG_SPLIT(split), on.handle));
   return y;
 }
 
@@ -265,8 +268,9 @@ c = bf16(prefix + delta) (prefix if ``delta`` is None; prefix [T, H] is
 updated in place otherwise), y = c * weight / sqrt(mean(c^2) + eps); the
 result is y in ``format``, from fp32.  ``norm_out`` [T, H] receives y in
 bf16 as well, if given.  H is a multiple of 32, at most 65536.)");
-  m.def("matmul", &matmul, "a"_a, "w"_a, "out"_a = py::none(), py::kw_only(), "pdl"_a = false,
-        "stream"_a = py::none(),
+  m.def("matmul", &matmul, "a"_a, "w"_a, "out"_a = py::none(), py::kw_only(), "pdl"_a = false, "kernel"_a = 0,
+        "split"_a = 0, "stream"_a = py::none(),
         R"(``a`` [m, k] times the transpose of ``w`` [n, k], of one format: bf16
-[m, n], fp32 sums (attn_res_mx_matmul).)");
+[m, n], fp32 sums (attn_res_mx_matmul).  ``kernel`` (KERNEL_NARROW,
+KERNEL_WIDE, KERNEL_WIDER) and ``split`` override the automatic choice.)");
 }

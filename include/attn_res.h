@@ -427,7 +427,21 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
  * [a->rows, w->rows] bf16 at out_row, for two matrices of one format and
  * width (a->cols == w->cols); fp32 sums on the tensor cores (tcgen05, block
  * scaled), rounded to bf16 once.  Any number of rows on both sides.
+ * Repeated calls give the same bits.
+ *
+ * Beside ATTN_RES_FLAG_PDL, flags takes tuning overrides (0 = automatic; the
+ * results do not depend on them beyond fp32 summation order):
+ *   KERNEL(k): ATTN_RES_MX_NARROW -- a CTA for 128 rows of w and up to 128 of
+ *              a, K split over a cluster (few tokens, or few tiles);
+ *              ATTN_RES_MX_WIDE, ATTN_RES_MX_WIDER -- persistent CTA pairs,
+ *              256 rows of a and 256 or 384 of w at a time;
+ *   SPLIT(s):  with ATTN_RES_MX_NARROW, the CTAs that share a tile's K: 1..6,
+ *              at most the 128-byte blocks of a row of codes.
+ * An override that cannot be met is ATTN_RES_EINVAL.
  */
+#define ATTN_RES_MX_NARROW 1
+#define ATTN_RES_MX_WIDE 2
+#define ATTN_RES_MX_WIDER 3
 attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t* w,
                                      attn_res_bf16_t* out, int64_t out_row, uint32_t flags,
                                      void* stream);

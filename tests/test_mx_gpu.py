@@ -352,16 +352,65 @@ PRODUCTS = [(1, 1, 32), (1, 128, 64), (2, 7, 96), (3, 129, 160), (15, 200, 224),
             (300, 2050, 352), (513, 300, 640), (700, 1030, 288), (1025, 513, 4128)]
 
 
+def k_blocks(fmt, K):
+    return -(-(K if fmt == "mxfp8" else K // 2) // 128)
+
+
+# Every form of the product: automatic; narrow with K whole, split in two and
+# as often as it can be; both wide ones.
+FORMS = {"auto": {}, "narrow1": dict(kernel=1, split=1), "narrow2": dict(kernel=1, split=2),
+         "narrow6": dict(kernel=1, split=6), "wide": dict(kernel=2), "wider": dict(kernel=3)}
+
+
+def form(name, fmt, K):
+    kw = dict(FORMS[name])
+    if "split" in kw:
+        kw["split"] = min(kw["split"], k_blocks(fmt, K))
+    return kw
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
 def test_product(fmt, M, N, K):
     a = random_matrix(M, K, fmt, 21, pad=16 if M % 2 else 0)
     w = random_matrix(N, K, fmt, 22, pad=32 if N % 2 else 0, scale=0.02)
-    out = Rows(M, N, 8 if N % 2 else 0)
-    mx.matmul(a.t, w.t, out.t)
-    torch.cuda.synchronize()
-    assert out.intact() and a.intact() and w.intact()
-    check_product(out.t, matrix_values(a), matrix_values(w), K)
+    va, vw = matrix_values(a), matrix_values(w)
+    for name in FORMS:
+        out = Rows(M, N, 8 if N % 2 else 0)
+        mx.matmul(a.t, w.t, out.t, **form(name, fmt, K))
+        torch.cuda.synchronize()
+        assert out.intact() and a.intact() and w.intact(), name
+        check_product(out.t, va, vw, K)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(2500, 2500, 1120), (777, 9001, 352), (20000, 96, 64), (257, 40000, 288)])
+def test_product_of_many_tiles(fmt, M, N, K):
+    """More tiles than CTAs at work: the persistent forms' walk and their ring."""
+    a, w = mx.quantize(activations(M, K, 31), fmt), mx.quantize((activations(N, K, 32) * 0.02).bfloat16(), fmt)
+
+    def vals(t):
+        return torch.from_numpy(R.values(t.data.view(torch.uint8).cpu().numpy(),
+                                         t.scales.view(torch.uint8).cpu().numpy().reshape(-1), fmt)).cuda()
+    va, vw = vals(a), vals(w)
+    for name in ("auto", "narrow1", "wide", "wider"):
+        check_product(mx.matmul(a, w, **form(name, fmt, K)), va, vw, K)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("off", [0, 8])
+def test_product_rows_off_sector_boundaries(fmt, off):
+    """Results whose rows start on 16-byte but not on 32-byte boundaries, and ragged ends."""
+    M, K = 300, 256
+    a = random_matrix(M, K, fmt, 33)
+    for N in (256, 261, 520):
+        w = random_matrix(N, K, fmt, 34)
+        for name in FORMS:
+            buf = torch.zeros(M, 536 + 8, dtype=torch.bfloat16, device="cuda")
+            out = buf[:, off:off + N]
+            mx.matmul(a.t, w.t, out, **form(name, fmt, K))
+            check_product(out, matrix_values(a), matrix_values(w), K)
+            assert not buf[:, :off].any() and not buf[:, off + N:].any(), name
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -380,9 +429,10 @@ def test_product_ignores_what_lies_behind(fmt, M):
             r = rows[behind]
             t[-1][:, r % 32, r // 32, :] = fill
             m.gd.view.view(m.rows, m.row_bytes)[:, m.used:] = 0x7F if fill else 0
-        outs.append(mx.matmul(a.t, w.t).clone())
-    assert torch.equal(outs[0], outs[1])
-    assert torch.isfinite(outs[0]).all()
+        outs.append([mx.matmul(a.t, w.t, **form(name, fmt, K)) for name in FORMS])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+        assert torch.isfinite(x).all()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -393,11 +443,12 @@ def test_product_of_nan_groups(fmt, M):
     x, v = activations(M, K, 25), activations(N, K, 26)
     x[M // 2, 100] = float("inf")
     v[7, 300] = float("nan")
-    out = mx.matmul(mx.quantize(x, fmt), mx.quantize(v, fmt))
     bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
     bad[M // 2, :] = True
     bad[:, 7] = True
-    assert torch.equal(torch.isnan(out), bad)
+    a, w = mx.quantize(x, fmt), mx.quantize(v, fmt)
+    for name in FORMS:
+        assert torch.equal(torch.isnan(mx.matmul(a, w, **form(name, fmt, K))), bad), name
 
 
 def test_product_tensor_scales():
@@ -428,9 +479,11 @@ def test_product_far_scales(fmt):
 @pytest.mark.parametrize("M", [1, 48, 129, 900])
 def test_product_is_repeatable(fmt, M):
     a, w = random_matrix(M, 1056, fmt, 29), random_matrix(700, 1056, fmt, 30)
-    first = mx.matmul(a.t, w.t)
-    for _ in range(5):
-        assert torch.equal(mx.matmul(a.t, w.t), first)
+    for name in FORMS:
+        kw = form(name, fmt, 1056)
+        first = mx.matmul(a.t, w.t, **kw)
+        for _ in range(5):
+            assert torch.equal(mx.matmul(a.t, w.t, **kw), first), name
 
 
 def test_zero_rows():
@@ -540,19 +593,21 @@ def test_layer_in_a_graph(T):
 
 
 def test_calls_in_flight_together():
-    """Products and conversions on four streams at once, every form of the product."""
+    """Products on five streams at once, every form among them."""
     cases = []
-    for i, (M, fmt) in enumerate([(1, "mxfp4"), (48, "nvfp4"), (150, "mxfp8"), (2000, "mxfp4")]):
+    for i, (M, fmt, name) in enumerate([(1, "mxfp4", "auto"), (48, "nvfp4", "narrow6"), (150, "mxfp8", "narrow2"),
+                                        (2000, "mxfp4", "wider"), (700, "nvfp4", "wide")]):
         a = mx.quantize(activations(M, 2048, 40 + i), fmt)
         w = mx.quantize(activations(1500, 2048, 50 + i), fmt)
-        cases.append((a, w, mx.matmul(a, w), torch.cuda.Stream()))
+        kw = form(name, fmt, 2048)
+        cases.append((a, w, kw, mx.matmul(a, w, **kw), torch.cuda.Stream()))
     torch.cuda.synchronize()
     got = [[] for _ in cases]
     for _ in range(8):
-        for k, (a, w, _o, s) in enumerate(cases):
-            got[k].append(mx.matmul(a, w, stream=s))
+        for k, (a, w, kw, _o, s) in enumerate(cases):
+            got[k].append(mx.matmul(a, w, stream=s, **kw))
     torch.cuda.synchronize()
-    for k, (_a, _w, o, _s) in enumerate(cases):
+    for k, (_a, _w, _kw, o, _s) in enumerate(cases):
         assert all(torch.equal(o, x) for x in got[k])
 
 
@@ -591,6 +646,14 @@ def test_binding_refusals():
         mx.add_rms_norm(x, x, x[0].clone())
     with pytest.raises(ValueError):
         mx.quantize(x, "mxfp5")
+    with pytest.raises(ar.AttnResError):
+        mx.matmul(q, q, kernel=4)
+    with pytest.raises(ar.AttnResError):
+        mx.matmul(q, q, kernel=mx.KERNEL_WIDE, split=2)
+    with pytest.raises(ValueError):
+        mx.matmul(q, q, split=-1)
+    with pytest.raises(TypeError):
+        mx.matmul(q, q.data)
 
 
 @pytest.mark.slow

@@ -155,7 +155,12 @@ def test_matmul_matrix_refusals(lib, change, status):
     (norm, dict(norm_out=addr(2)), 3), (norm, dict(flags=4), 1),
     (matmul, dict(out=0), 1), (matmul, dict(out_row=64), 1), (matmul, dict(out=addr(0, 4)), 2),
     (matmul, dict(out_row=76), 2), (matmul, dict(out=addr(1)), 3), (matmul, dict(out=addr(2, 1024)), 3),
-    (matmul, dict(out=addr(2, 1 << 32)), 3), (matmul, dict(flags=1 << 16), 1),
+    (matmul, dict(out=addr(2, 1 << 32)), 3), (matmul, dict(flags=2), 1),
+    (matmul, dict(flags=ar.FLAG_KERNEL(4)), 1), (matmul, dict(flags=ar.FLAG_STAGES(2)), 1),
+    (matmul, dict(flags=ar.FLAG_SPLIT(1)), 1), (matmul, dict(flags=ar.FLAG_KERNEL(2) | ar.FLAG_SPLIT(1)), 1),
+    (matmul, dict(flags=ar.FLAG_KERNEL(1) | ar.FLAG_SPLIT(2)), 1),  # one block of K
+    (matmul, dict(flags=ar.FLAG_KERNEL(1) | ar.FLAG_SPLIT(7), a=matrix(1, cols=8192),
+                  w=matrix(2, rows=70, cols=8192)), 1),
 ])
 def test_refusals(lib, call, change, status):
     assert call(**change) == status
