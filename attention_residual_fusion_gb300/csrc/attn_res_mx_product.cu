@@ -170,24 +170,25 @@ cudaError_t launch_wide(const ProductCall& c) {
 }
 
 // The forms' times in units of 10 ns, for the choice between them, from graph
-// replays on GB300 of 1..8192 tokens x 1024..16384 columns x 2048..8192 (all
-// formats, inputs in L2).  A pair of the wide form takes 1.1 us and 0.32 us
-// for each 128-byte block of K for a tile of 256 columns, 2.5 us and 0.40 us
+// replays on GB300 of 1..8192 tokens x 1024..16384 columns x 1024..8192 (all
+// formats, inputs in L2).  A pair of the wide form takes 0.8 us and 0.34 us
+// for each 128-byte block of K for a tile of 256 columns, 1.75 us and 0.40 us
 // for one of 384; 76 pairs work at once; 6 us for the launch, the first loads
 // and the last stores.  The narrow form's 128-token tiles take in 34 KB for
 // each block, about 10 TB/s in all, and 5.5 us for the rest:
-//   tokens x columns x K       narrow     wide 256   wide 384
-//   128 x 7168 x 7168 mxfp4    12.3 us    15.2 us        -
-//   300 x 2050 x 7200 mxfp8    14.5       24.9           -
-//   256 x 7168 x 7168 mxfp4    16.7       15.4           -
-//   512 x 7168 x 7168 mxfp4    21.1       16.0       19.1 us
-//   1024 x 7168 x 7168 mxfp4     -        26.4       19.9
-//   8192 x 7168 x 7168 mxfp4     -       129        114
-//   4096 x 16384 x 2048 nvfp4    -        55.2       61.6
+//   tokens x columns x K       narrow     wide      wider
+//   128 x 7168 x 7168 mxfp4    12.1 us    15.2 us        -
+//   300 x 2050 x 7200 mxfp8    14.5       25.3      30.0 us
+//   256 x 7168 x 7168 mxfp4    14.8       15.6      18.5
+//   512 x 7168 x 7168 mxfp4    17.2       16.2      19.1
+//   1024 x 7168 x 7168 mxfp4   31.1       26.7      20.2
+//   8192 x 8192 x 1024 mxfp4     -        36.2      41.4
+//   4096 x 16384 x 2048 nvfp4    -        55.2      55.1
+//   8192 x 7168 x 7168 mxfp4     -       129       109
 int64_t wide_cost(const ProductCall& c, int64_t blocks, int tile_columns) {
   const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + tile_columns - 1) / tile_columns);
   const int64_t waves = (tiles + 75) / 76;
-  return 600 + waves * (tile_columns == 256 ? 110 + 32 * blocks : 250 + 40 * blocks);
+  return 600 + waves * (tile_columns == 256 ? 80 + 34 * blocks : 175 + 40 * blocks);
 }
 int64_t narrow_cost(const ProductCall& c, int64_t blocks) {
   const int64_t tiles = (c.a->rows + 127) / 128 * ((c.w->rows + 127) / 128);

@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(192, 2)
 // holds 128 tokens' rows, half of the weight rows (the instruction reads the
 // other half from the peer) and the scales of its tokens and of all TN weight
 // rows.  Persistent pairs walk the tiles; warp 0 loads, warp 1 of the first
-// CTA issues the MMAs of both, warps 4..11 drain the accumulators through
-// registers to global memory.
+// CTA issues the MMAs of both, the warps from 4 on drain the accumulators
+// through registers to global memory.
 //
 // What bounds a tile is what an SM takes in (measured: 60 bytes a clock of
 // the 64 its port has) more than the tensor cores, so wide tiles:
@@ -569,34 +569,38 @@ __device__ __forceinline__ void tile_at(const TileWalk& w, int i, int& mt, int& 
   mt = band * kBand + j - nt * rows;
 }
 
-// Stores 64 fp32 columns (from `col` on) of a lane's row as bf16, straight from
-// its registers: 32 bytes, a whole sector, at a time where the rows lie on
-// 32-byte boundaries.  (Through shared memory and bulk tensor stores the same
-// bytes passed shared memory twice, whose bandwidth the operands need.)
-__device__ __forceinline__ void store_row64(const ProductParams& p, const uint32_t (&r)[64], float scale,
-                                            int64_t row, int col, bool wide) {
+// 64 fp32 columns of a thread's row as bf16 pairs.
+__device__ __forceinline__ void pack64(const uint32_t (&r)[64], float scale, uint32_t (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    v[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
+}
+// Stores 64 columns (from `col` on) of a lane's row, straight from its
+// registers: 32 bytes, a whole sector, at a time where the rows lie on 32-byte
+// boundaries.  (Through shared memory and bulk tensor stores the same bytes
+// pass shared memory twice, whose bandwidth the operands need: 4096 x 16384 x
+// 2048 nvfp4 61 us instead of 56, 8192 x 7168 x 7168 mxfp4 115 either way.)
+__device__ __forceinline__ void store_row64(const ProductParams& p, const uint32_t (&v)[32], int64_t row, int col,
+                                            bool wide) {
   uint16_t* const o = p.out + row * p.out_row + col;
   const int left = (int)p.n - col;  // columns that exist
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = pack_bf16x2(__uint_as_float(r[16 * k + 2 * e]) * scale, __uint_as_float(r[16 * k + 2 * e + 1]) * scale);
     uint16_t* const at = o + 16 * k;
     if (left >= 16 * k + 16) {
       if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[0]), "r"(v[1]),
-                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[8 * k]),
+                     "r"(v[8 * k + 1]), "r"(v[8 * k + 2]), "r"(v[8 * k + 3]), "r"(v[8 * k + 4]),
+                     "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
                      : "memory");
       } else {
-        st_row(at, make_uint4(v[0], v[1], v[2], v[3]));
-        st_row(at + 8, make_uint4(v[4], v[5], v[6], v[7]));
+        st_row(at, make_uint4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]));
+        st_row(at + 8, make_uint4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]));
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        if (16 * k + e < left) at[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+        if (16 * k + e < left) at[e] = (uint16_t)(v[8 * k + e / 2] >> (16 * (e % 2)));
     }
   }
 }
@@ -736,6 +740,11 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
       int mt, nt;
       tile_at(walk, i, mt, nt);
       const int64_t row = (int64_t)mt * C::TM + rank * 128 + 32 * q + lane;
+      // HALVES = 2: both accumulators into registers, each released, before the
+      // stores (with each accumulator's stores at once the second was released
+      // 2500 clocks later: 8192 x 7168 x 7168 mxfp4 114 us instead of 109)
+      uint32_t v[2][32];
+      int local[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (HALVES == 2 || h == 0) {
@@ -745,16 +754,20 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
         }
         // 64 columns: of accumulator h, or first of the 128 that successive
         // accumulators share (the upper of the first, the lower of the second)
-        const int local = HALVES == 2 ? h * C::HN + 64 * part
-                                      : ((tile & 1) == (h == 0 ? 0u : 1u) ? 128 : 0) + 64 * part;
+        local[h] = HALVES == 2 ? h * C::HN + 64 * part
+                               : ((tile & 1) == (h == 0 ? 0u : 1u) ? 128 : 0) + 64 * part;
         uint32_t r[64];
-        tmem_ld64(lanes + (HALVES == 2 ? 0 : (tile & 1) * C::ACC_STEP) + local, r);
+        tmem_ld64(lanes + (HALVES == 2 ? 0 : (tile & 1) * C::ACC_STEP) + local[h], r);
         tmem_ld_wait(r);
         tmem_fence_before();
         __syncwarp();
         if ((HALVES == 2 || h == 0) && lane == 0) mbar_arrive_remote(map_rank(acc_empty + 8 * h, 0));
-        if (!failed && row < p.m) store_row64(p, r, scale, row, nt * C::TN + local, wide);
+        pack64(r, scale, v[h]);
+        if (HALVES == 1 && !failed && row < p.m) store_row64(p, v[h], row, nt * C::TN + local[h], wide);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (HALVES == 2 && !failed && row < p.m) store_row64(p, v[h], row, nt * C::TN + local[h], wide);
       if (i + step >= tiles) grid_dep_launch_dependents();
     }
   }
