@@ -12,6 +12,7 @@
 
 #include "attn_res.h"
 #include "attn_res_launch.cuh"
+#include "attn_res_mx.cuh"
 
 namespace {
 
@@ -365,8 +366,9 @@ StreamLaunchFn lookup_stream(int S, int shape, bool d, bool o) {
 }
 
 // Self-test of the bounded waits: one warp waits, with the same code the
-// mixture kernels use, on an mbarrier that nothing ever arrives at; the wait
-// must give up after limit_ns and record the stage time-out bit.
+// mixture kernels use and then with that of the microscaled product, on an
+// mbarrier that nothing ever arrives at; every wait must give up after
+// limit_ns, and the stage time-out bit is recorded.
 __global__ void attn_res_selftest_wait_kernel(unsigned* err, uint64_t limit_ns) {
   __shared__ __align__(8) unsigned long long bar;
   if (threadIdx.x == 0) {
@@ -374,8 +376,11 @@ __global__ void attn_res_selftest_wait_kernel(unsigned* err, uint64_t limit_ns) 
     attn_res_dev::fence_mbar_init();
   }
   __syncthreads();
-  if (!attn_res_dev::mbar_wait_bounded(attn_res_dev::smem_addr(&bar), 0u, limit_ns) &&
-      threadIdx.x == 0)
+  const uint32_t b = attn_res_dev::smem_addr(&bar);
+  const bool passed = attn_res_dev::mbar_wait_bounded(b, 0u, limit_ns) ||
+                      attn_res_dev::phase_wait<false>(b, 0u, limit_ns) ||
+                      attn_res_dev::phase_wait<true>(b, 0u, limit_ns);
+  if (!passed && threadIdx.x == 0)
     atomicOr(err, attn_res_dev::kErrStageTimeout);
 }
 
