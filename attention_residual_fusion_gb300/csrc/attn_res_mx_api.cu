@@ -99,17 +99,20 @@ attn_res_status_t launched(cudaError_t e) {
   return ATTN_RES_ECUDA;
 }
 
+// A programmatic launch: the kernel's start-up overlaps the end of a preceding
+// kernel that lets its dependents start, and it waits for that kernel before
+// it touches memory.
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
-  Launch(int64_t grid, int threads, uint32_t flags, void* stream) {
+  Launch(int64_t grid, int threads, void* stream) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = &attr;
-    cfg.numAttrs = (flags & ATTN_RES_FLAG_PDL) ? 1 : 0;
+    cfg.numAttrs = 1;
   }
   Launch(const Launch&) = delete;
 };
@@ -141,7 +144,7 @@ attn_res_status_t run_rows(Kern pick, const attn_res_bf16_t* x, int64_t x_row, c
   p.col_chunks = static_cast<uint32_t>(chunks);
   p.jobs = static_cast<uint32_t>(jobs);
   const int64_t ctas = (jobs + kMxThreads / 32 - 1) / (kMxThreads / 32);
-  Launch l(ctas, kMxThreads, flags, stream);
+  Launch l(ctas, kMxThreads, stream);
   return launched(cudaLaunchKernelEx(&l.cfg, pick(q->format), p));
 }
 
@@ -248,7 +251,7 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
   const int64_t nv = p.q.group_tiles * 4 * mx_group(q->format) / 8;
   const NormShape shape = norm_shape(q->format, nv, T);
   const int64_t pad_rows = (T + 127) / 128 * 128 - T;
-  Launch l(T + (pad_rows + kMxPadRows - 1) / kMxPadRows, shape.threads, flags, stream);
+  Launch l(T + (pad_rows + kMxPadRows - 1) / kMxPadRows, shape.threads, stream);
   return launched(cudaLaunchKernelEx(&l.cfg, shape.kernel, p));
 }
 

@@ -71,6 +71,7 @@ ProductParams params(const ProductCall& c) {
   p.n = c.w->rows;
   p.group_tiles = mx_group_tiles(FMT, c.a->cols);
   p.row_bytes_used = (int)(c.a->cols * mx_bits(FMT) / 8);
+  p.early_weights = c.pdl;
   p.err = c.err;
   return p;
 }
@@ -87,6 +88,9 @@ cudaError_t allow_smem(Kern kern, uint32_t bytes, int device, std::atomic<uint64
   return cudaSuccess;
 }
 
+// Every launch is a programmatic one: its start-up overlaps the end of a
+// preceding kernel that lets its dependents start (those of this library do,
+// after their own wait), and it waits for that kernel before it touches memory.
 struct Attributes {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
@@ -101,7 +105,7 @@ struct Attributes {
     cfg.dynamicSmemBytes = smem;
     cfg.stream = c.stream;
     cfg.attrs = attr;
-    cfg.numAttrs = c.pdl ? 2 : 1;
+    cfg.numAttrs = 2;
   }
   Attributes(const Attributes&) = delete;
 };

@@ -238,6 +238,7 @@ struct ProductParams {
   int64_t m, n;          // rows of a and of w
   int64_t group_tiles;   // scale tiles along a row
   int row_bytes_used;    // bytes of a row's codes
+  bool early_weights;    // w may be read before the preceding kernel is complete
   unsigned* err;
 };
 
@@ -334,13 +335,18 @@ __global__ void __launch_bounds__(192, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2 * S + 1; ++i) mbar_init(full + 8 * i, 1);
     fence_mbar_init();
-    // the weights do not depend on the preceding kernel: the first stages'
-    // are on their way before the wait for it
-    for (int i = 0; i < ahead; ++i) load_w(i, i);
+    // with ATTN_RES_FLAG_PDL the weights do not depend on the preceding kernel:
+    // the first stages' are on their way before the wait for it
+    if (p.early_weights)
+      for (int i = 0; i < ahead; ++i) load_w(i, i);
   }
   grid_dep_wait();
   if (threadIdx.x == 0)
-    for (int i = 0; i < ahead; ++i) load_a(i, i);
+    for (int i = 0; i < ahead; ++i) {
+      if (!p.early_weights) load_w(i, i);
+      load_a(i, i);
+    }
+  // (TMEM only now: while the preceding kernel runs it may need it itself)
   if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), C::COLS);
   tmem_fence_before();
   __syncthreads();
@@ -593,16 +599,17 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
     mbar_init(drained, 1);
     fence_mbar_init();
   }
+  grid_dep_wait();
+  // (TMEM only now: while the preceding kernel runs it may need it itself)
   if (warp == 1) tmem_alloc<2>(smem_addr(&tmem_slot), C::COLS);
   tmem_fence_before();
-  __syncthreads();
-  cluster_sync();
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers and TMEM are there
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
   const int tiles = walk.m_tiles * walk.n_tiles;
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
   const int blocks = (p.row_bytes_used + 127) / 128;
-  grid_dep_wait();
 
   if (warp == 0 && lane == 0) {
     bool failed = false;

@@ -35,9 +35,9 @@ __global__ void __launch_bounds__(kMxThreads, 6) attn_res_mx_quantize_kernel(con
   using M = Mx<FMT>;
   const int lane = threadIdx.x & 31;
   const uint32_t job = blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
+  grid_dep_wait();
   const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   const float g6 = 6.f * g;
-  grid_dep_wait();
   if (job < p.jobs) {
     const uint32_t rest = job / p.col_chunks;
     const int r = (int)(rest & 31);
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kMxThreads) attn_res_mx_dequantize_kernel(cons
   using M = Mx<FMT>;
   const int lane = threadIdx.x & 31;
   const uint32_t job = blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
-  const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   grid_dep_wait();
+  const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   if (job < p.jobs) {
     const uint32_t rest = job / p.col_chunks;
     const int r = (int)(rest & 31);
@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
     return;
   }
   uint4 w[VPT], c[VPT];
+  grid_dep_wait();
   const float g = M::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
   const float g6 = 6.f * g;
-  grid_dep_wait();
   uint16_t* const prow = p.prefix + t * p.prefix_row;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {

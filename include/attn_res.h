@@ -383,15 +383,18 @@ int64_t attn_res_mx_scale_bytes(int format, int64_t rows, int64_t cols);
 
 /*
  * The calls below take device pointers of the current device and enqueue on
- * `stream` as attn_res does; flags is 0 or ATTN_RES_FLAG_PDL (weight and
- * tensor-scale arguments, and attn_res_mx_matmul's w, may then be read before
- * the preceding kernel has finished; everything else is read, and everything
- * is written, after it).  bf16 rows have unit inner stride, 16-byte aligned
- * pointers and row strides that are multiples of 8 elements and >= the row
- * width.  A written range that overlaps another argument's is
- * ATTN_RES_EALIAS; the other errors are as for attn_res, before any launch.
- * With no rows (for the product: no rows in a or in w) a call checks the
- * scalar arguments and returns OK.
+ * `stream` as attn_res does.  They are launched so that a kernel's start-up
+ * overlaps the end of a preceding kernel that lets its dependents start, and
+ * touch no memory before that kernel is complete: fully stream ordered.  flags
+ * is 0 or ATTN_RES_FLAG_PDL, which lets attn_res_mx_matmul read w before then
+ * (the contract of that flag, with w in the place of the bank rows; the other
+ * calls take the flag and do as without it).
+ *
+ * bf16 rows have unit inner stride, 16-byte aligned pointers and row strides
+ * that are multiples of 8 elements and >= the row width.  A written range that
+ * overlaps another argument's is ATTN_RES_EALIAS; the other errors are as for
+ * attn_res, before any launch.  With no rows (for the product: no rows in a or
+ * in w) a call checks the scalar arguments and returns OK.
  */
 
 /* q = x [q->rows, q->cols] in q's format; writes q's data and scales. */
