@@ -245,7 +245,7 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
   p.delta_row = delta_row;
   p.norm_row = norm_row;
   p.eps = eps;
-  p.inv_h = 1.0f / static_cast<float>(H);
+  p.width = static_cast<float>(H);
   p.q = view(*q);
   // vectors of the row, with the groups that fill its last scale tile
   const int64_t nv = p.q.group_tiles * 4 * mx_group(q->format) / 8;

@@ -134,7 +134,7 @@ struct MxNormParams {
   const uint16_t* weight;
   uint16_t* norm_out;
   int64_t prefix_row, delta_row, norm_row;
-  float eps, inv_h;
+  float eps, width;  // width: H
   MxView q;
 };
 
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
   __syncthreads();
   const int warps = blockDim.x >> 5;
   const float tot = warp_sum(lane < warps ? part[lane] : 0.f);
-  const float rstd = __frsqrt_rn(fmaf(tot, p.inv_h, p.eps));
+  // (the quotient itself: 1 / H as a factor would put its rounding into every row)
+  const float rstd = __frsqrt_rn(tot / p.width + p.eps);
   const f32x2 r2 = f2_make(rstd, rstd);
   uint8_t* const qrow = p.q.data + t * p.q.row_bytes;
   uint8_t* const srow =
