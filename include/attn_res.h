@@ -369,7 +369,7 @@ attn_res_status_t attn_res_tp_finish(int64_t Hs, int64_t H, attn_res_bf16_t* pre
 
 typedef struct {
   int32_t format;            /* ATTN_RES_MXFP8, ATTN_RES_MXFP4 or ATTN_RES_NVFP4 */
-  int64_t rows, cols;        /* rows >= 0; cols > 0, a multiple of 32 */
+  int64_t rows, cols;        /* 0 <= rows <= 2^31 - 256; 0 < cols <= 2^30, a multiple of 32 */
   void* data;                /* element codes */
   int64_t row_bytes;         /* between rows of data */
   uint8_t* scales;           /* tiled scales */
@@ -377,8 +377,8 @@ typedef struct {
                                 NULL unless format is ATTN_RES_NVFP4 */
 } attn_res_mx_t;
 
-/* Bytes of the scale buffer; -1 for an unknown format, rows < 0, or cols not
- * a positive multiple of 32 (or too large for the product to fit). */
+/* Bytes of the scale buffer; -1 for an unknown format, or rows or cols out of
+ * the ranges above. */
 int64_t attn_res_mx_scale_bytes(int format, int64_t rows, int64_t cols);
 
 /*
