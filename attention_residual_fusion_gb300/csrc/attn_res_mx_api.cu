@@ -148,34 +148,57 @@ attn_res_status_t run_rows(Kern pick, const attn_res_bf16_t* x, int64_t x_row, c
   return launched(cudaLaunchKernelEx(&l.cfg, pick(q->format), p));
 }
 
-// The norm's launch for a row of `nv` vectors.
+// The norm's launch for `rows` rows of `nv` vectors (with the groups that fill
+// the last scale tile).
 struct NormShape {
   void (*kernel)(MxNormParams);
   int threads;
+  int64_t ctas;
 };
-template <int VPT, int MAX_THREADS, int MIN_CTAS>
-NormShape norm_shape(int format, int64_t nv) {
+template <int VPT, int MAX_THREADS, int MIN_CTAS, bool WARP_ROWS>
+NormShape norm_shape(int format, int64_t nv, int64_t rows) {
   NormShape s;
-  s.threads = static_cast<int>(((nv + VPT - 1) / VPT + 31) / 32 * 32);
+  const int64_t padded = (rows + 127) / 128 * 128;
+  if (WARP_ROWS) {
+    s.threads = 32 * kMxWarpRows;
+    s.ctas = padded / kMxWarpRows;
+  } else {
+    s.threads = static_cast<int>(((nv + VPT - 1) / VPT + 31) / 32 * 32);
+    s.ctas = rows + (padded - rows + kMxPadRows - 1) / kMxPadRows;
+  }
   switch (format) {
-    case ATTN_RES_MXFP8: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP8, VPT, MAX_THREADS, MIN_CTAS>; break;
-    case ATTN_RES_MXFP4: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP4, VPT, MAX_THREADS, MIN_CTAS>; break;
-    default: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_NVFP4, VPT, MAX_THREADS, MIN_CTAS>; break;
+    case ATTN_RES_MXFP8: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP8, VPT, MAX_THREADS, MIN_CTAS, WARP_ROWS>; break;
+    case ATTN_RES_MXFP4: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_MXFP4, VPT, MAX_THREADS, MIN_CTAS, WARP_ROWS>; break;
+    default: s.kernel = attn_res_mx_norm_kernel<ATTN_RES_NVFP4, VPT, MAX_THREADS, MIN_CTAS, WARP_ROWS>; break;
   }
   return s;
 }
-// Vectors per thread by the row's width, and for rows of 4097..8192 columns by
-// their number: with few, more threads a row (H = 7168, T = 1 / 256: 2.4 / 4.7
-// us with 2 vectors each against 2.8 / 4.9 with 4); with many, four CTAs an SM
-// of 4 vectors a thread keep the most bytes on their way (T = 8192: 64.8 us,
-// 94 % of the copy rate; 78.7 with 2 vectors, 80.4 with two larger CTAs).
+// Vectors per thread by the rows' number and width.  With few rows, more
+// threads a row.  With many (from kNormManyRows on), up to 1024 columns a warp a
+// row -- CTAs of a warp or two would start no faster than an SM takes CTAs --
+// and above, four vectors a thread at 64 registers, which keeps the most bytes
+// of rows on their way.  Graph replay, mxfp8 with an addend, us (few / many):
+//   rows x H         few    many         rows x H         few    many
+//   256 x 512        1.65   1.83         8192 x 512       9.25   5.28
+//   512 x 4096       3.10   3.29         8192 x 2048     22.9   20.8
+//   512 x 7168       5.99   5.35         8192 x 4096     40.1   37.9
+//   1024 x 1024      2.64   2.20         8192 x 7168     78.3   63.3
+//   1024 x 4096      6.07   5.72         (95 % of the copy rate)
+//   1024 x 7168     11.1    9.28
+constexpr int64_t kNormManyRows = 1024;
 NormShape norm_shape(int format, int64_t nv, int64_t rows) {
-  if (nv <= 256) return norm_shape<1, 256, 1>(format, nv);
-  if (nv <= 512) return norm_shape<2, 256, 1>(format, nv);
-  if (nv <= 1024 && rows < 1024) return norm_shape<2, 512, 2>(format, nv);
-  if (nv <= 1024) return norm_shape<4, 256, 4>(format, nv);
-  if (nv <= 4096) return norm_shape<8, 512, 1>(format, nv);
-  return norm_shape<8, 1024, 1>(format, nv);
+  if (rows >= kNormManyRows) {
+    if (nv <= 32) return norm_shape<1, 256, 1, true>(format, nv, rows);
+    if (nv <= 64) return norm_shape<2, 256, 1, true>(format, nv, rows);
+    if (nv <= 128) return norm_shape<4, 256, 1, true>(format, nv, rows);
+    if (nv <= 256) return norm_shape<4, 64, 16, false>(format, nv, rows);
+    if (nv <= 512) return norm_shape<4, 128, 8, false>(format, nv, rows);
+    if (nv <= 1024) return norm_shape<4, 256, 4, false>(format, nv, rows);
+  }
+  if (nv <= 256) return norm_shape<1, 256, 1, false>(format, nv, rows);
+  if (nv <= 1024) return norm_shape<2, 512, 2, false>(format, nv, rows);
+  if (nv <= 4096) return norm_shape<8, 512, 1, false>(format, nv, rows);
+  return norm_shape<8, 1024, 1, false>(format, nv, rows);
 }
 
 }  // namespace
@@ -247,11 +270,8 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
   p.eps = eps;
   p.width = static_cast<float>(H);
   p.q = view(*q);
-  // vectors of the row, with the groups that fill its last scale tile
-  const int64_t nv = p.q.group_tiles * 4 * mx_group(q->format) / 8;
-  const NormShape shape = norm_shape(q->format, nv, T);
-  const int64_t pad_rows = (T + 127) / 128 * 128 - T;
-  Launch l(T + (pad_rows + kMxPadRows - 1) / kMxPadRows, shape.threads, stream);
+  const NormShape shape = norm_shape(q->format, p.q.group_tiles * 4 * mx_group(q->format) / 8, T);
+  Launch l(shape.ctas, shape.threads, stream);
   return launched(cudaLaunchKernelEx(&l.cfg, shape.kernel, p));
 }
 

@@ -124,9 +124,11 @@ __global__ void __launch_bounds__(kMxThreads) attn_res_mx_dequantize_kernel(cons
 // One CTA per token row, the row in registers (VPT 16-byte vectors per
 // thread); the sum of c^2 takes one CTA barrier.  CTAs behind the last row
 // write the zero scale entries of the rows that pad the last 128-row tile,
-// kPadRows of them each.
+// kMxPadRows of them each.  With WARP_ROWS, for many narrow rows, a warp takes
+// a row (or one of the padding rows) and no barrier is needed.
 constexpr int kMxNormMaxThreads = 1024;
 constexpr int kMxPadRows = 8;
+constexpr int kMxWarpRows = 8;  // warps of a CTA with WARP_ROWS
 
 struct MxNormParams {
   uint16_t* prefix;
@@ -138,21 +140,24 @@ struct MxNormParams {
   MxView q;
 };
 
-template <int FMT, int VPT, int MAX_THREADS, int MIN_CTAS>
+template <int FMT, int VPT, int MAX_THREADS, int MIN_CTAS, bool WARP_ROWS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
     attn_res_mx_norm_kernel(const MxNormParams p) {
   using M = Mx<FMT>;
   __shared__ float part[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = WARP_ROWS ? 32 : blockDim.x;  // threads of a row
+  const int tid = WARP_ROWS ? lane : threadIdx.x;
+  const int64_t t = WARP_ROWS ? (int64_t)blockIdx.x * kMxWarpRows + warp : (int64_t)blockIdx.x;
   const int nv = (int)(p.q.cols / 8);
   if (t >= p.q.rows) {
     grid_dep_wait();
     grid_dep_launch_dependents();
-    const int64_t first = p.q.rows + (t - p.q.rows) * kMxPadRows;
+    constexpr int kRows = WARP_ROWS ? 1 : kMxPadRows;
+    const int64_t first = p.q.rows + (t - p.q.rows) * kRows;
     const int64_t last = (p.q.rows + 127) / 128 * 128;
-    for (int64_t row = first; row < first + kMxPadRows && row < last; ++row)
-      for (int64_t a = tid; a < p.q.group_tiles; a += blockDim.x)
+    for (int64_t row = first; row < first + kRows && row < last; ++row)
+      for (int64_t a = tid; a < p.q.group_tiles; a += team)
         *reinterpret_cast<uint32_t*>(p.q.scales + ((row / 128) * p.q.group_tiles + a) * 512 +
                                      (row % 32) * 16 + (row % 128) / 32 * 4) = 0u;
     return;
@@ -164,14 +169,14 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
   uint16_t* const prow = p.prefix + t * p.prefix_row;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int i = tid + v * blockDim.x;
+    const int i = tid + v * team;
     c[v] = i < nv ? ld_row(prow + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
   }
   if (p.delta) {
     uint4 d[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      const int i = tid + v * blockDim.x;
+      const int i = tid + v * team;
       d[v] = i < nv ? ld_row(p.delta + t * p.delta_row + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
   // after the addend, whose registers they take
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int i = tid + v * blockDim.x;
+    const int i = tid + v * team;
     w[v] = i < nv ? ld_weight(p.weight + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
   }
   f32x2 sq2 = f2_make(0.f, 0.f);
@@ -193,11 +198,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
       sq2 = f2_fma(x, x, sq2);
     }
   }
-  const float sq = warp_sum(f2_lo(sq2) + f2_hi(sq2));
-  if (lane == 0) part[warp] = sq;
-  __syncthreads();
-  const int warps = blockDim.x >> 5;
-  const float tot = warp_sum(lane < warps ? part[lane] : 0.f);
+  float tot = warp_sum(f2_lo(sq2) + f2_hi(sq2));
+  if constexpr (!WARP_ROWS) {
+    if (lane == 0) part[warp] = tot;
+    __syncthreads();
+    tot = warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
+  }
   // (the quotient itself: 1 / H as a factor would put its rounding into every row)
   const float rstd = __frsqrt_rn(tot / p.width + p.eps);
   const f32x2 r2 = f2_make(rstd, rstd);
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
       p.q.scales + (t / 128) * p.q.group_tiles * 512 + (t % 32) * 16 + (t % 128) / 32 * 4;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int i = tid + v * blockDim.x;
+    const int i = tid + v * team;
     const bool in_row = i < nv;
     f32x2 y[4];
     uint32_t am = 0;

@@ -282,6 +282,14 @@ def test_norm(fmt, T, H, pad):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,H", [(1024, 32), (1025, 288), (1100, 512), (1033, 992), (1151, 1056), (1030, 2048),
+                                 (1027, 2080), (1024, 4096), (1026, 4128), (1025, 7168), (1024, 8224)])
+def test_norm_of_many_rows(fmt, T, H):
+    """The shapes for many rows, a warp a row among them."""
+    check_norm(T, H, fmt, True, 8 if T % 2 else 0, bool(T % 3), 15, g=0.004 if fmt == "nvfp4" else None)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("scale,eps", [(1e-3, 1e-6), (1e-3, 0.0), (100.0, 1e-5), (1e-15, 1e-6)])
 def test_norm_scales(fmt, scale, eps):
     check_norm(9, 512, fmt, True, 0, True, 13, scale, eps)
