@@ -546,33 +546,53 @@ __device__ __forceinline__ void pack64(const uint32_t (&r)[64], float scale, uin
   for (int k = 0; k < 32; ++k)
     v[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
 }
+// COUNT of them from FIRST on, `left` of which exist.
+template <int FIRST, int COUNT>
+__device__ __forceinline__ void store_piece(uint16_t* o, const uint32_t (&v)[32], int left) {
+  uint16_t* const at = o + FIRST;
+  constexpr int k = FIRST / 2;
+  if (left >= FIRST + COUNT) {
+    if constexpr (COUNT == 16)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[k]), "r"(v[k + 1]),
+                   "r"(v[k + 2]), "r"(v[k + 3]), "r"(v[k + 4]), "r"(v[k + 5]), "r"(v[k + 6]), "r"(v[k + 7])
+                   : "memory");
+    else
+      st_row(at, make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < COUNT; ++e)
+      if (FIRST + e < left) at[e] = (uint16_t)(v[k + e / 2] >> (16 * (e % 2)));
+  }
+}
+
 // Stores 64 columns (from `col` on) of a lane's row, straight from its
-// registers: 32 bytes, a whole sector, at a time where the rows lie on 32-byte
-// boundaries.  (Through shared memory and bulk tensor stores the same bytes
-// pass shared memory twice, whose bandwidth the operands need: 4096 x 16384 x
-// 2048 nvfp4 61 us instead of 56, 8192 x 7168 x 7168 mxfp4 115 either way.)
+// registers: 32 bytes, a whole sector, at a time, after half a sector where the
+// row lies between two of them; `wide`: none of the rows does, which a full
+// tile then need not look at (2 % of a product's time).  (Half sectors alone: 1361 x 14008 x 864 mxfp8
+// 28.4 us instead of 19.9.  Through shared memory and bulk tensor stores the same
+// bytes pass shared memory twice, whose bandwidth the operands need: 4096 x
+// 16384 x 2048 nvfp4 61 us instead of 56, 8192 x 7168 x 7168 mxfp4 115 either
+// way.)
 __device__ __forceinline__ void store_row64(const ProductParams& p, const uint32_t (&v)[32], int64_t row, int col,
                                             bool wide) {
   uint16_t* const o = p.out + row * p.out_row + col;
   const int left = (int)p.n - col;  // columns that exist
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint16_t* const at = o + 16 * k;
-    if (left >= 16 * k + 16) {
-      if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[8 * k]),
-                     "r"(v[8 * k + 1]), "r"(v[8 * k + 2]), "r"(v[8 * k + 3]), "r"(v[8 * k + 4]),
-                     "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
-                     : "memory");
-      } else {
-        st_row(at, make_uint4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]));
-        st_row(at + 8, make_uint4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]));
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (16 * k + e < left) at[e] = (uint16_t)(v[8 * k + e / 2] >> (16 * (e % 2)));
-    }
+  if (wide && left >= 64) {
+    store_piece<0, 16>(o, v, 64);
+    store_piece<16, 16>(o, v, 64);
+    store_piece<32, 16>(o, v, 64);
+    store_piece<48, 16>(o, v, 64);
+  } else if ((reinterpret_cast<uintptr_t>(o) & 16u) == 0) {
+    store_piece<0, 16>(o, v, left);
+    store_piece<16, 16>(o, v, left);
+    store_piece<32, 16>(o, v, left);
+    store_piece<48, 16>(o, v, left);
+  } else {
+    store_piece<0, 8>(o, v, left);
+    store_piece<8, 16>(o, v, left);
+    store_piece<24, 16>(o, v, left);
+    store_piece<40, 16>(o, v, left);
+    store_piece<56, 8>(o, v, left);
   }
 }
 

@@ -212,7 +212,9 @@ at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bo
     y = *out;
     row = row_stride(y, 8);
   } else {
-    row = (n + 7) / 8 * 8;  // rows start on 16-byte boundaries, whatever n
+    // rows start on 16-byte boundaries, whatever n; where they are padded
+    // anyway, on 32-byte ones (the wide forms then store whole sectors)
+    row = n % 8 == 0 ? n : (n + 15) / 16 * 16;
     y = new_tensor({m, row}, at::kBFloat16, device);
     if (row != n) y = y.narrow(1, 0, n);
   }

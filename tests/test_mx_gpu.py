@@ -422,6 +422,25 @@ def test_product_rows_off_sector_boundaries(fmt, off):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("N", [8, 73, 200, 505, 520, 776])
+def test_product_rows_on_and_off_sector_boundaries(fmt, N):
+    """Every other row of the result between two 32-byte boundaries."""
+    M, K = 300, 256
+    a, w = random_matrix(M, K, fmt, 35), random_matrix(N, K, fmt, 36)
+    for name in FORMS:
+        out = Rows(M, N)
+        if out.row % 16 == 0:
+            out = Rows(M, N, 8)
+        mx.matmul(a.t, w.t, out.t, **form(name, fmt, K))
+        torch.cuda.synchronize()
+        assert out.intact(), name
+        check_product(out.t, matrix_values(a), matrix_values(w), K)
+        # rows that the call makes itself start on 16-byte boundaries
+        y = mx.matmul(a.t, w.t, **form(name, fmt, K))
+        assert y.shape == (M, N) and y.stride(0) % 8 == 0 and torch.equal(y, out.t), name
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M", [1, 5, 40, 130, 600])
 def test_product_ignores_what_lies_behind(fmt, M):
     """NaN scale codes of rows that do not exist and codes behind a row's end
