@@ -49,42 +49,65 @@ int64_t row_stride(const at::Tensor& t, int64_t to) {
   return t.size(0) > 1 ? t.stride(0) : (t.size(1) + to - 1) / to * to;
 }
 
-struct MxTensor {
-  at::Tensor data, scales;
-  OptTensor global_scale;
-  attn_res_mx_t c = {};
-
-  MxTensor(at::Tensor d, at::Tensor s, int f, OptTensor g, int64_t rows, int64_t cols)
-      : data(std::move(d)), scales(std::move(s)), global_scale(std::move(g)) {
-    c.format = f;
-    c.rows = rows;
-    c.cols = cols;
-    c.data = data.data_ptr();
-    c.row_bytes = row_stride(data, 16);
-    c.scales = static_cast<uint8_t*>(scales.data_ptr());
-    c.tensor_scale = global_scale ? static_cast<const float*>(global_scale->data_ptr()) : nullptr;
-  }
-  at::Device device() const { return data.device(); }
-};
+// The address of a tensor's first element.  A storage can shrink under its
+// tensors (untyped_storage().resize_()): elements outside it have no address.
+void* address(const char* name, const at::Tensor& t) {
+  if (t.numel() == 0) return t.data_ptr();
+  int64_t last = t.storage_offset();
+  for (int64_t d = 0; d < t.dim(); ++d) last += (t.size(d) - 1) * t.stride(d);
+  if ((static_cast<size_t>(last) + 1) * t.element_size() > t.storage().nbytes())
+    refuse(std::string(name) + "'s storage does not hold its elements");
+  return t.data_ptr();
+}
 
 void check_global_scale(int f, const OptTensor& g, at::Device device) {
   if (g && (f != ATTN_RES_NVFP4 || g->scalar_type() != at::kFloat || g->numel() != 1 || g->device() != device))
     refuse("global_scale must be one float32 beside the data (nvfp4 only)");
 }
 
+// The tensors are the caller's too, who may give them other storage, sizes or
+// types between two calls: addresses, strides and sizes are taken, and the
+// parts checked, at each call.
+struct MxTensor {
+  at::Tensor data, scales;
+  OptTensor global_scale;
+  int format;
+
+  int64_t rows() const { return data.size(0); }
+  int64_t cols() const { return data.size(1) * (format == ATTN_RES_MXFP8 ? 1 : 2); }
+  at::Device device() const { return data.device(); }
+
+  void check() const {
+    if (data.scalar_type() != data_type(format) || data.dim() != 2 || !data.is_cuda() ||
+        (data.stride(1) != 1 && data.size(1) > 1))
+      refuse(std::string("data must be a CUDA ") + c10::toString(data_type(format)) +
+             " matrix with unit inner stride");
+    const auto shape = scales_shape(format, rows(), cols());
+    if (scales.scalar_type() != scales_type(format) || scales.device() != data.device() ||
+        scales.sizes() != at::IntArrayRef(shape) || !scales.is_contiguous())
+      refuse(std::string("scales must be a contiguous ") + c10::toString(scales_type(format)) +
+             " tensor of scales_shape(format, rows, cols) beside data");
+    check_global_scale(format, global_scale, data.device());
+  }
+
+  attn_res_mx_t matrix() const {
+    check();
+    attn_res_mx_t c = {};
+    c.format = format;
+    c.rows = rows();
+    c.cols = cols();
+    c.data = address("data", data);
+    c.row_bytes = row_stride(data, 16);
+    c.scales = static_cast<uint8_t*>(address("scales", scales));
+    c.tensor_scale = global_scale ? static_cast<const float*>(address("global_scale", *global_scale)) : nullptr;
+    return c;
+  }
+};
+
 MxTensor make(const at::Tensor& data, const at::Tensor& scales, const std::string& format, const OptTensor& g) {
-  const int f = format_code(format);
-  if (data.scalar_type() != data_type(f) || data.dim() != 2 || !data.is_cuda() ||
-      (data.stride(1) != 1 && data.size(1) > 1))
-    refuse(std::string("data must be a CUDA ") + c10::toString(data_type(f)) + " matrix with unit inner stride");
-  const int64_t rows = data.size(0), cols = data.size(1) * (f == ATTN_RES_MXFP8 ? 1 : 2);
-  const auto shape = scales_shape(f, rows, cols);
-  if (scales.scalar_type() != scales_type(f) || scales.device() != data.device() ||
-      scales.sizes() != at::IntArrayRef(shape) || !scales.is_contiguous())
-    refuse(std::string("scales must be a contiguous ") + c10::toString(scales_type(f)) +
-           " tensor of scales_shape(format, rows, cols) beside data");
-  check_global_scale(f, g, data.device());
-  return MxTensor(data, scales, f, g, rows, cols);
+  MxTensor t{data, scales, g, format_code(format)};
+  t.check();
+  return t;
 }
 
 void check_shape(int64_t rows, int64_t cols) {
@@ -94,8 +117,8 @@ void check_shape(int64_t rows, int64_t cols) {
 MxTensor allocate(int64_t rows, int64_t cols, int f, const OptTensor& g, at::Device device) {
   check_shape(rows, cols);
   check_global_scale(f, g, device);
-  return MxTensor(new_tensor({rows, f == ATTN_RES_MXFP8 ? cols : cols / 2}, data_type(f), device),
-                  new_tensor(scales_shape(f, rows, cols), scales_type(f), device), f, g, rows, cols);
+  return {new_tensor({rows, f == ATTN_RES_MXFP8 ? cols : cols / 2}, data_type(f), device),
+          new_tensor(scales_shape(f, rows, cols), scales_type(f), device), g, f};
 }
 
 void check_rows(const char* name, const at::Tensor& t) {
@@ -109,7 +132,9 @@ void check_rows(const char* name, const at::Tensor& t, int64_t rows, int64_t col
     refuse(std::string(name) + " must be a [" + std::to_string(rows) + ", " + std::to_string(cols) + "] matrix");
   if (t.device() != device) refuse("all tensors of a call must be on one device");
 }
-attn_res_bf16_t* bf16(const at::Tensor& t) { return static_cast<attn_res_bf16_t*>(t.data_ptr()); }
+attn_res_bf16_t* bf16(const char* name, const at::Tensor& t) {
+  return static_cast<attn_res_bf16_t*>(address(name, t));
+}
 
 // The device and stream of a call: current while outputs are allocated and the
 // kernel is launched.
@@ -143,19 +168,19 @@ uint32_t flags_of(bool pdl) { return pdl ? ATTN_RES_FLAG_PDL : 0u; }
 
 // The result of a quantising call: `out`, checked, or a new one.
 py::object result(const py::object& out, int64_t rows, int64_t cols, const std::string& format, const OptTensor& g,
-                  at::Device device, const attn_res_mx_t** c) {
+                  at::Device device, attn_res_mx_t* c) {
   const int f = format_code(format);
   if (out.is_none()) {
     py::object made = py::cast(allocate(rows, cols, f, g, device));
-    *c = &made.cast<MxTensor&>().c;
+    *c = made.cast<const MxTensor&>().matrix();
     return made;
   }
   const MxTensor& o = out.cast<const MxTensor&>();
-  if (o.c.format != f || (g && !(o.global_scale && g->is_same(*o.global_scale))))
+  if (o.format != f || (g && !(o.global_scale && g->is_same(*o.global_scale))))
     refuse("out has another format or global_scale");
-  if (o.c.rows != rows || o.c.cols != cols || o.device() != device)
+  *c = o.matrix();
+  if (c->rows != rows || c->cols != cols || o.device() != device)
     refuse("out must be an MxTensor of the rows' shape, on their device");
-  *c = &o.c;
   return out;
 }
 
@@ -163,17 +188,18 @@ py::object quantize(const at::Tensor& x, const std::string& format, const OptTen
                     const py::object& out, bool pdl, const py::object& stream) {
   check_rows("x", x);
   const On on(x.device(), stream);
-  const attn_res_mx_t* c;
+  attn_res_mx_t c;
   py::object q = result(out, x.size(0), x.size(1), format, global_scale, x.device(), &c);
-  check(attn_res_mx_quantize(bf16(x), row_stride(x, 8), c, flags_of(pdl), on.handle));
+  check(attn_res_mx_quantize(bf16("x", x), row_stride(x, 8), &c, flags_of(pdl), on.handle));
   return q;
 }
 
 at::Tensor dequantize(const MxTensor& q, const OptTensor& out, bool pdl, const py::object& stream) {
+  const attn_res_mx_t c = q.matrix();
   const On on(q.device(), stream);
-  if (out) check_rows("out", *out, q.c.rows, q.c.cols, q.device());
-  at::Tensor x = out ? *out : new_tensor({q.c.rows, q.c.cols}, at::kBFloat16, q.device());
-  check(attn_res_mx_dequantize(&q.c, bf16(x), row_stride(x, 8), flags_of(pdl), on.handle));
+  if (out) check_rows("out", *out, c.rows, c.cols, q.device());
+  at::Tensor x = out ? *out : new_tensor({c.rows, c.cols}, at::kBFloat16, q.device());
+  check(attn_res_mx_dequantize(&c, bf16("out", x), row_stride(x, 8), flags_of(pdl), on.handle));
   return x;
 }
 
@@ -189,20 +215,21 @@ py::object add_rms_norm(const at::Tensor& prefix, const OptTensor& delta, const 
       weight.size(0) != cols || !weight.is_contiguous())
     refuse("weight must be a contiguous bfloat16 [H] tensor beside prefix");
   const On on(device, stream);
-  const attn_res_mx_t* c;
+  attn_res_mx_t c;
   py::object q = result(out, rows, cols, format, global_scale, device, &c);
-  check(attn_res_mx_norm(bf16(prefix), row_stride(prefix, 8), delta ? bf16(*delta) : nullptr,
-                         delta ? row_stride(*delta, 8) : 0, bf16(weight), static_cast<float>(eps),
-                         norm_out ? bf16(*norm_out) : nullptr, norm_out ? row_stride(*norm_out, 8) : 0, c,
-                         flags_of(pdl), on.handle));
+  check(attn_res_mx_norm(bf16("prefix", prefix), row_stride(prefix, 8), delta ? bf16("delta", *delta) : nullptr,
+                         delta ? row_stride(*delta, 8) : 0, bf16("weight", weight), static_cast<float>(eps),
+                         norm_out ? bf16("norm_out", *norm_out) : nullptr, norm_out ? row_stride(*norm_out, 8) : 0,
+                         &c, flags_of(pdl), on.handle));
   return q;
 }
 
 at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bool pdl, int kernel, int split,
                   const py::object& stream) {
+  const attn_res_mx_t ca = a.matrix(), cw = w.matrix();
   const at::Device device = a.device();
-  const int64_t m = a.c.rows, n = w.c.rows;
-  if (a.c.format != w.c.format || a.c.cols != w.c.cols) refuse("a and w must have one format and one width");
+  const int64_t m = ca.rows, n = cw.rows;
+  if (ca.format != cw.format || ca.cols != cw.cols) refuse("a and w must have one format and one width");
   if (w.device() != device) refuse("all tensors of a call must be on one device");
   const On on(device, stream);
   at::Tensor y;
@@ -219,7 +246,7 @@ at::Tensor matmul(const MxTensor& a, const MxTensor& w, const OptTensor& out, bo
     if (row != n) y = y.narrow(1, 0, n);
   }
   if (kernel < 0 || kernel > 15 || split < 0 || split > 255) refuse("no such kernel or split");
-  check(attn_res_mx_matmul(&a.c, &w.c, bf16(y), row,
+  check(attn_res_mx_matmul(&ca, &cw, bf16("out", y), row,
                            flags_of(pdl) | ATTN_RES_FLAG_KERNEL(kernel) | ATTN_RES_FLAG_SPLIT(split), on.handle));
   return y;
 }
@@ -233,7 +260,9 @@ PYBIND11_MODULE(_mx, m) {
 data: [rows, cols] float8_e4m3fn ("mxfp8") or [rows, cols // 2] uint8 (two
 e2m1 codes a byte, the even column low), unit inner stride; scales:
 ``scales_shape(format, rows, cols)``, contiguous, float8_e8m0fnu or (nvfp4)
-float8_e4m3fn; global_scale: one fp32 on the device, nvfp4 only, or None.)")
+float8_e4m3fn; global_scale: one fp32 on the device, nvfp4 only, or None.
+Every call takes and checks the three tensors as they then are, so they may be
+given other storage in between; one whose storage is gone is refused.)")
       .def(py::init(&make), "data"_a, "scales"_a, "format"_a, "global_scale"_a = py::none())
       .def_static(
           "empty",
@@ -250,8 +279,8 @@ float8_e4m3fn; global_scale: one fp32 on the device, nvfp4 only, or None.)")
       .def_property_readonly("data", [](const MxTensor& t) { return t.data; })
       .def_property_readonly("scales", [](const MxTensor& t) { return t.scales; })
       .def_property_readonly("global_scale", [](const MxTensor& t) { return t.global_scale; })
-      .def_property_readonly("format", [](const MxTensor& t) { return format_name(t.c.format); })
-      .def_property_readonly("shape", [](const MxTensor& t) { return std::make_tuple(t.c.rows, t.c.cols); })
+      .def_property_readonly("format", [](const MxTensor& t) { return format_name(t.format); })
+      .def_property_readonly("shape", [](const MxTensor& t) { return std::make_tuple(t.rows(), t.cols()); })
       .def_property_readonly("device", [](const MxTensor& t) { return t.device(); });
   m.def("quantize", &quantize, "x"_a, "format"_a = "mxfp4", "global_scale"_a = py::none(), "out"_a = py::none(),
         py::kw_only(), "pdl"_a = false, "stream"_a = py::none(),
