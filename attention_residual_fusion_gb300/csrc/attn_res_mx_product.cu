@@ -110,23 +110,88 @@ struct Attributes {
   Attributes(const Attributes&) = delete;
 };
 
-// CTAs that share a tile's K in the narrow form: two CTAs an SM (of 152) if
-// that fills at least three quarters of them, else one (so that no SM has twice
-// the work of another); at most 6 (clusters of 8 measured slower than of 4..6
-// wherever they fit: 128 tokens x 2048 x 4096 9.3 us against 7.6, 64 x 4096 x
-// 7168 8.8 against 7.4) and a block of K each.
-int64_t narrow_split(int64_t tiles, int64_t blocks) {
-  auto per_sm = [&](int64_t ctas) {
-    const int64_t s = ctas / tiles;
-    return s > kMaxSplit ? kMaxSplit : s < 1 ? 1 : s;
-  };
-  int64_t s = per_sm(304);
-  if (s * tiles < 228) s = per_sm(152);
-  return s < blocks ? s : blocks;
+// The choice of form and split: each one's time by a model of it, in units of
+// 10 ns, whose constants were fitted to 414 products behind another small call
+// of the library (graph replays on GB300, inputs in L2: 1..8192 tokens x
+// 64..16384 columns x 32..8192, all formats, every form and split).  Over these
+// the choice takes 0.6 % longer than the best form in the geometric mean, and
+// 15 % at most; over 125 others 0.8 % and 11 %.
+//
+// Narrow form: waves of clusters.  A wave that leaves an SM a single CTA takes
+// less for each 128-byte block of K and for the joining of the parts than one
+// with two; more than 64 tokens (tiles of 128) cost more in all of these.
+// Clusters of three and more leave some SMs without a second CTA: kClusters[s]
+// of s CTAs run at once on GB300's 152 SMs, and as a second wave the rest
+// takes as long again (3200 x 512 x 2368 mxfp8 in three parts, 100 clusters,
+// 16.4 us; whole 10.0).  (Counted by the driver for a kernel of this shape
+// without TMEM; for one that takes TMEM it counts a CTA an SM, whatever the
+// columns.)
+constexpr int kSms = 152;
+constexpr int kClusters[kMaxSplit + 1] = {0, 304, 152, 97, 74, 58, 46};
+struct NarrowCosts {
+  int base;             // launch, first loads, results
+  int block, block2;    // a CTA's block of K: one CTA an SM, two
+  int two;              // two CTAs an SM: first loads and results
+  int join, join2;      // joining: one CTA an SM, two
+  int join2_part;       // two: for each part
+  int wave;             // a wave before the last one
+};
+constexpr NarrowCosts kNarrowFew = {220, 28, 28, 65, 50, 55, 28, 173};    // up to 64 tokens
+constexpr NarrowCosts kNarrowMany = {420, 26, 46, 128, 105, 151, 0, 410};  // tiles of 128 tokens
+int64_t narrow_cost(const NarrowCosts& k, int64_t tiles, int64_t blocks, int split) {
+  const int64_t per_cta = (blocks + split - 1) / split, clusters = kClusters[split];
+  const int64_t waves = (tiles + clusters - 1) / clusters;
+  const bool two = (tiles - (waves - 1) * clusters) * split > kSms;
+  int64_t t = k.base + (waves - 1) * (k.wave + k.block2 * per_cta);
+  t += two ? k.two + k.block2 * per_cta : k.block * per_cta;
+  if (split > 1) t += two ? k.join2 + k.join2_part * split : k.join;
+  return t;
+}
+// Wide forms: waves of pairs, a tile's blocks of K, and the way of all results
+// to memory (34000 of them take 10 ns at the copy rate).
+//   tokens x columns x K        narrow     wide      wider   (us, the small call's 1.3 us taken off)
+//   300 x 2050 x 7200 mxfp8      12.8      23.2       27.6
+//   128 x 7168 x 7168 mxfp4      10.2      13.9       16.8
+//   256 x 7168 x 7168 mxfp4      12.2      14.0       16.9
+//   512 x 7168 x 7168 mxfp4      15.3      14.3       16.9
+//   1024 x 7168 x 7168 mxfp4     28.8      24.7       18.4
+//   4096 x 256 x 1024 mxfp4       5.3       6.0        7.0
+//   4096 x 4096 x 128 mxfp4      18.1      11.6       12.9
+//   8192 x 16384 x 128 mxfp4      125      61.2       63.5
+//   8192 x 7168 x 32 nvfp4       61.2      31.2       29.4
+struct WideCosts {
+  int base, tile, block;
+  int results;  // for 34000 results, in hundredths
+};
+constexpr WideCosts kWide = {372, 51, 36, 62}, kWider = {364, 77, 43, 88};
+int64_t wide_cost(const WideCosts& k, const ProductCall& c, int64_t blocks, int tile_columns, int64_t pairs) {
+  const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + tile_columns - 1) / tile_columns);
+  const int64_t waves = (tiles + pairs - 1) / pairs;
+  return k.base + waves * (k.tile + k.block * blocks) + c.a->rows * c.w->rows / 34000 * k.results / 100;
+}
+
+// Token tiles of the narrow form's grid (its y).
+constexpr int64_t kNarrowMaxRows = int64_t(65535) * 128;
+int64_t k_blocks(const attn_res_mx_t& a) { return (a.cols * mx_bits(a.format) / 8 + 127) / 128; }
+
+// The least cost of the splits 1..kMaxSplit, and that split.
+int64_t plan_narrow(const ProductCall& c, int tile_tokens, int64_t blocks, int* split) {
+  const int64_t tiles = (c.w->rows + 127) / 128 * ((c.a->rows + tile_tokens - 1) / tile_tokens);
+  const NarrowCosts& k = tile_tokens == 128 ? kNarrowMany : kNarrowFew;
+  int64_t least = narrow_cost(k, tiles, blocks, 1);
+  *split = 1;
+  for (int s = 2; s <= kMaxSplit && s <= blocks; ++s) {
+    const int64_t t = narrow_cost(k, tiles, blocks, s);
+    if (t < least) {
+      least = t;
+      *split = s;
+    }
+  }
+  return least;
 }
 
 template <int FMT, int TN>
-cudaError_t launch_narrow(const ProductCall& c) {
+cudaError_t launch_narrow(const ProductCall& c, int split) {
   using C = NarrowCfg<FMT, TN>;
   void (*kern)(ProductParams, CUtensorMap, CUtensorMap) = attn_res_mx_product_narrow_kernel<FMT, TN>;
   static std::atomic<uint64_t> enabled{0};
@@ -137,90 +202,74 @@ cudaError_t launch_narrow(const ProductCall& c) {
   if (e != cudaSuccess) return e;
   const ProductParams p = params<FMT>(c);
   const int64_t n_tiles = (p.n + 127) / 128, m_tiles = (p.m + TN - 1) / TN;
-  const int blocks = (p.row_bytes_used + 127) / 128;
-  const int64_t split = c.split ? c.split : narrow_split(n_tiles * m_tiles, blocks);
   Attributes l(dim3((unsigned)(n_tiles * split), (unsigned)m_tiles, 1), C::THREADS, C::SMEM, (unsigned)split, c);
   return cudaLaunchKernelEx(&l.cfg, kern, p, map_a, map_w);
 }
 
 template <int FMT, int HALVES>
-cudaError_t launch_wide(const ProductCall& c) {
+struct Wide {
   using C = WideCfg<FMT, HALVES>;
-  void (*kern)(ProductParams, TileWalk, WideMaps) = attn_res_mx_product_wide_kernel<FMT, HALVES>;
-  static std::atomic<uint64_t> enabled{0};
-  static std::atomic<int> pairs_of[64];
-  cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
-  WideMaps maps;
-  if (e == cudaSuccess) e = operand_map(*c.a, 128, &maps.a);
-  if (e == cudaSuccess) e = operand_map(*c.w, C::HN / 2, &maps.w);
-  if (e == cudaSuccess) e = scales_map(*c.a, C::F::ATOMS, &maps.a_sf);
-  if (e == cudaSuccess) e = scales_map(*c.w, C::F::ATOMS, &maps.w_sf);
-  if (e != cudaSuccess) return e;
-  const ProductParams p = params<FMT>(c);
-  const int64_t m_tiles = (p.m + C::TM - 1) / C::TM, n_tiles = (p.n + C::TN - 1) / C::TN;
-  const int64_t tiles = m_tiles * n_tiles;
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-  const TileWalk walk{(int)m_tiles, (int)n_tiles};
-  Attributes l(dim3(2, 1, 1), C::THREADS, C::SMEM, 2, c);
-  int pairs = pairs_of[c.device].load(std::memory_order_acquire);
-  if (pairs == 0) {  // that the device holds at once
-    e = cudaOccupancyMaxActiveClusters(&pairs, kern, &l.cfg);
+  static constexpr auto kern = attn_res_mx_product_wide_kernel<FMT, HALVES>;
+
+  // Pairs that the device holds at once.
+  static cudaError_t resident(const ProductCall& c, int* pairs) {
+    static std::atomic<uint64_t> enabled{0};
+    static std::atomic<int> known[64];
+    *pairs = known[c.device].load(std::memory_order_acquire);
+    if (*pairs != 0) return cudaSuccess;
+    cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
+    const Attributes l(dim3(2, 1, 1), C::THREADS, C::SMEM, 2, c);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(pairs, kern, &l.cfg);
     if (e != cudaSuccess) return e;
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
-    pairs_of[c.device].store(pairs, std::memory_order_release);
+    if (*pairs < 1) return cudaErrorInvalidConfiguration;
+    known[c.device].store(*pairs, std::memory_order_release);
+    return cudaSuccess;
   }
-  l.cfg.gridDim.x = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-  return cudaLaunchKernelEx(&l.cfg, kern, p, walk, maps);
-}
-
-// The forms' times in units of 10 ns, for the choice between them, from graph
-// replays on GB300 of 1..8192 tokens x 1024..16384 columns x 1024..8192 (all
-// formats, inputs in L2).  A pair of the wide form takes 0.8 us and 0.34 us
-// for each 128-byte block of K for a tile of 256 columns, 1.75 us and 0.40 us
-// for one of 384; 76 pairs work at once; 6 us for the launch, the first loads
-// and the last stores.  The narrow form's 128-token tiles take in 34 KB for
-// each block, about 10 TB/s in all, and 5.5 us for the rest:
-//   tokens x columns x K       narrow     wide      wider
-//   128 x 7168 x 7168 mxfp4    12.1 us    15.2 us        -
-//   300 x 2050 x 7200 mxfp8    14.5       25.3      30.0 us
-//   256 x 7168 x 7168 mxfp4    14.8       15.6      18.5
-//   512 x 7168 x 7168 mxfp4    17.2       16.2      19.1
-//   1024 x 7168 x 7168 mxfp4   31.1       26.7      20.2
-//   8192 x 8192 x 1024 mxfp4     -        36.2      41.4
-//   4096 x 16384 x 2048 nvfp4    -        55.2      55.1
-//   8192 x 7168 x 7168 mxfp4     -       129       109
-int64_t wide_cost(const ProductCall& c, int64_t blocks, int tile_columns) {
-  const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + tile_columns - 1) / tile_columns);
-  const int64_t waves = (tiles + 75) / 76;
-  return 600 + waves * (tile_columns == 256 ? 80 + 34 * blocks : 175 + 40 * blocks);
-}
-int64_t narrow_cost(const ProductCall& c, int64_t blocks) {
-  const int64_t tiles = (c.a->rows + 127) / 128 * ((c.w->rows + 127) / 128);
-  return 550 + tiles * blocks * 34 / 100;
-}
-
-// Token tiles of the narrow form's grid (its y).
-constexpr int64_t kNarrowMaxRows = int64_t(65535) * 128;
-int64_t k_blocks(const attn_res_mx_t& a) { return (a.cols * mx_bits(a.format) / 8 + 127) / 128; }
+  static cudaError_t launch(const ProductCall& c, int pairs) {
+    WideMaps maps;
+    cudaError_t e = operand_map(*c.a, 128, &maps.a);
+    if (e == cudaSuccess) e = operand_map(*c.w, C::HN / 2, &maps.w);
+    if (e == cudaSuccess) e = scales_map(*c.a, C::F::ATOMS, &maps.a_sf);
+    if (e == cudaSuccess) e = scales_map(*c.w, C::F::ATOMS, &maps.w_sf);
+    if (e != cudaSuccess) return e;
+    const int64_t m_tiles = (c.a->rows + C::TM - 1) / C::TM, n_tiles = (c.w->rows + C::TN - 1) / C::TN;
+    const int64_t tiles = m_tiles * n_tiles;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const TileWalk walk{(int)m_tiles, (int)n_tiles};
+    Attributes l(dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs), 1, 1), C::THREADS, C::SMEM, 2, c);
+    return cudaLaunchKernelEx(&l.cfg, kern, params<FMT>(c), walk, maps);
+  }
+};
 
 template <int FMT>
 cudaError_t launch_format(const ProductCall& c) {
+  using One = Wide<FMT, 1>;
+  using Two = Wide<FMT, 2>;
   const int64_t rows = c.a->rows, blocks = k_blocks(*c.a);
-  int kernel = c.kernel;
+  const int tile_tokens = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  int kernel = c.kernel, split = c.split, one_pairs = 0, two_pairs = 0;
+  int64_t narrow = INT64_MAX;
+  // up to 64 tokens the narrow form's time is that of reading the weights
+  if (kernel == 0 && rows <= 64) kernel = ATTN_RES_MX_NARROW;
+  if (split == 0 && (kernel == 0 ? rows <= kNarrowMaxRows : kernel == ATTN_RES_MX_NARROW))
+    narrow = plan_narrow(c, tile_tokens, blocks, &split);
+  cudaError_t e = cudaSuccess;
+  if (kernel == 0 || kernel == ATTN_RES_MX_WIDE) e = One::resident(c, &one_pairs);
+  if (e == cudaSuccess && (kernel == 0 || kernel == ATTN_RES_MX_WIDER)) e = Two::resident(c, &two_pairs);
+  if (e != cudaSuccess) return e;
   if (kernel == 0) {
-    const int64_t one = wide_cost(c, blocks, 256), two = wide_cost(c, blocks, 384);
-    // up to 64 tokens the narrow form's time is that of reading the weights
-    if (rows <= 64 || (rows <= kNarrowMaxRows && narrow_cost(c, blocks) < (one < two ? one : two)))
-      kernel = ATTN_RES_MX_NARROW;
-    else
-      kernel = one <= two ? ATTN_RES_MX_WIDE : ATTN_RES_MX_WIDER;
+    const int64_t one = wide_cost(kWide, c, blocks, 256, one_pairs);
+    const int64_t two = wide_cost(kWider, c, blocks, 384, two_pairs);
+    kernel = narrow < (one < two ? one : two) ? ATTN_RES_MX_NARROW : one <= two ? ATTN_RES_MX_WIDE : ATTN_RES_MX_WIDER;
   }
-  if (kernel == ATTN_RES_MX_WIDE) return launch_wide<FMT, 1>(c);
-  if (kernel == ATTN_RES_MX_WIDER) return launch_wide<FMT, 2>(c);
-  if (rows <= 16) return launch_narrow<FMT, 16>(c);
-  if (rows <= 32) return launch_narrow<FMT, 32>(c);
-  if (rows <= 64) return launch_narrow<FMT, 64>(c);
-  return launch_narrow<FMT, 128>(c);
+  if (kernel == ATTN_RES_MX_WIDE) return One::launch(c, one_pairs);
+  if (kernel == ATTN_RES_MX_WIDER) return Two::launch(c, two_pairs);
+  switch (tile_tokens) {
+    case 16: return launch_narrow<FMT, 16>(c, split);
+    case 32: return launch_narrow<FMT, 32>(c, split);
+    case 64: return launch_narrow<FMT, 64>(c, split);
+    default: return launch_narrow<FMT, 128>(c, split);
+  }
 }
 
 }  // namespace

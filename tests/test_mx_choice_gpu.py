@@ -1,0 +1,69 @@
+"""The product's automatic form and split, timed against every form that can be asked for."""
+import pytest
+import torch
+
+import attention_residual_fusion_gb300 as ar
+from attention_residual_fusion_gb300 import _build, mx
+from tests.test_mx_gpu import activations, k_blocks
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    ar.device_status(clear=True)
+    yield
+    assert ar.device_status() == 0
+
+
+def replay_us(call, calls=10, repeats=9):
+    """Median time of a call among others in a replayed graph."""
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(calls):
+            call()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    times = []
+    for _ in range(repeats):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / calls)
+    return sorted(times)[repeats // 2]
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [
+    # short K with many results: what the results and a tile's fixed work take decides
+    ("mxfp8", 8192, 16384, 32), ("mxfp4", 8192, 7168, 256), ("nvfp4", 4096, 4096, 128), ("mxfp8", 2048, 8192, 128),
+    # clusters of which a few would not run in the first wave
+    ("mxfp8", 3200, 512, 2368), ("mxfp8", 256, 3200, 3840),
+    # few tokens, a decode batch, a prefill
+    ("mxfp4", 1, 7168, 7168), ("nvfp4", 64, 4096, 7168), ("mxfp8", 300, 2048, 7200), ("mxfp4", 2048, 4096, 4096),
+])
+def test_automatic_form_is_near_the_best(fmt, M, N, K):
+    """Behind another small call of the library, as in a layer; a quarter is
+    left for noise and for the choice's model (15 % over 414 products at most)."""
+    a = mx.quantize(activations(M, K, 90), fmt)
+    w = mx.quantize((activations(N, K, 91) * 0.02).bfloat16(), fmt)
+    x = activations(1, 32, 92)
+    q = mx.quantize(x, fmt)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+
+    def timed(**kw):
+        def call():
+            mx.quantize(x, fmt, out=q)
+            mx.matmul(a, w, out, **kw)
+        return replay_us(call)
+
+    splits = range(1, min(6, k_blocks(fmt, K)) + 1) if M * N <= 1 << 21 else [1]
+    forms = [dict(kernel=mx.KERNEL_NARROW, split=s) for s in splits]
+    forms += [dict(kernel=mx.KERNEL_WIDE), dict(kernel=mx.KERNEL_WIDER)]
+    times = {tuple(f.values()): timed(**f) for f in forms}
+    auto = timed()
+    assert auto <= 1.25 * min(times.values()), (auto, times)
