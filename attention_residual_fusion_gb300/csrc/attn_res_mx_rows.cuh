@@ -17,7 +17,8 @@ namespace attn_res_dev {
 // entries of rows and groups that do not exist come out as zeros by the same
 // stores.  Four 16-byte loads per lane are in flight, and six CTAs an SM: on
 // 8192 x 7168 28.2 us to mxfp8, 25.4 to mxfp4 (86 % of the copy rate), 34.4 to
-// nvfp4, whose quotients bound it (with 8 CTAs 30.6, 26.2 and 36.1: spills).
+// nvfp4, whose quotients bound it and which spills 16 bytes a thread (with 8
+// CTAs 30.6, 26.2 and 36.1: all three spill, and more).
 constexpr int kMxThreads = 256;
 constexpr int kMxWarpCols = 256;
 
@@ -140,6 +141,113 @@ struct MxNormParams {
   MxView q;
 };
 
+// Eight elements of a normalised row (vector i, its eight products y) into q,
+// with the group's scale; every lane takes part, those past the row's end too.
+template <int FMT>
+__device__ __forceinline__ void norm_store(const MxNormParams& p, int64_t t, int i, bool in_row, const f32x2 (&y)[4],
+                                           float g, float g6) {
+  using M = Mx<FMT>;
+  uint32_t am = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) am = max(am, max(abs_bits(f2_lo(y[k])), abs_bits(f2_hi(y[k]))));
+  // past the row's end nothing counts, whatever the row's statistics make of 0
+  if (!in_row) am = 0;
+  const GroupScale<FMT> s = group_scale<FMT>(group_max<M::LANES>(am), g, g6);
+  if (in_row) {
+    st_codes<FMT>(p.q.data + t * p.q.row_bytes, i, encode8<FMT>(y, s));
+    if (p.norm_out)
+      st_row(p.norm_out + t * p.norm_row + (int64_t)i * 8,
+             make_uint4(pack_bf16x2(f2_lo(y[0]), f2_hi(y[0])), pack_bf16x2(f2_lo(y[1]), f2_hi(y[1])),
+                        pack_bf16x2(f2_lo(y[2]), f2_hi(y[2])), pack_bf16x2(f2_lo(y[3]), f2_hi(y[3]))));
+  }
+  const uint32_t word = scale_word<FMT>(in_row ? s.code : 0u);
+  const int atom = i / M::ATOM_LANES;
+  if ((threadIdx.x & 31) % M::ATOM_LANES == 0 && atom < p.q.group_tiles)
+    *reinterpret_cast<uint32_t*>(p.q.scales + ((t / 128) * p.q.group_tiles + atom) * 512 + (t % 32) * 16 +
+                                 (t % 128) / 32 * 4) = word;
+}
+
+// A row whose mean square (with eps) fp32 does not hold: it overflows, from
+// values of 2^64 / sqrt(H) on, or lies below this, where squares lose bits to
+// underflow.
+constexpr float kMxLeastMean = 0x1p-100f;
+
+// Such a row, from memory again: scaled by the power of two that brings its
+// largest value to 2^30 (less where eps counts) before the statistics are
+// taken.  y is the same function of the scaled row and of eps times the
+// scale's square, and the scaled values are exact but for those whose y lies
+// below 2^-156 times the weight.  (Reading the row again costs the other rows
+// no registers; with the scaling in the registers' copy 8192 x 7168 took 64.7
+// us to mxfp8 instead of 63.4.)  `part` is shared by the row's threads.
+template <int FMT, bool WARP_ROWS>
+__device__ __forceinline__ void norm_scaled_row(const MxNormParams& p, int64_t t, float* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = WARP_ROWS ? 32 : blockDim.x;
+  const int tid = WARP_ROWS ? lane : threadIdx.x;
+  const int nv = (int)(p.q.cols / 8);
+  const float g = Mx<FMT>::NV ? tensor_scale_of(p.q.tensor_scale) : 1.f;
+  uint16_t* const prow = p.prefix + t * p.prefix_row;
+  auto current = [&](int i) {
+    if (i >= nv) return make_uint4(0, 0, 0, 0);
+    const uint4 c = ld_row(prow + (int64_t)i * 8);
+    return p.delta ? add_bf16x8(c, ld_row(p.delta + t * p.delta_row + (int64_t)i * 8)) : c;
+  };
+  uint32_t am = 0;  // largest |c|, as a bf16 pattern
+#pragma unroll 1
+  for (int i = tid; i < nv; i += team) {
+    const uint4 c = current(i);
+    const uint32_t m = amax_pair(c, c);
+    am = max(am, max(m & 0xffffu, m >> 16));
+  }
+  am = __reduce_max_sync(0xffffffffu, am);
+  if constexpr (!WARP_ROWS) {
+    __syncthreads();
+    if (lane == 0) part[warp] = __uint_as_float(am);
+    __syncthreads();
+    am = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? __float_as_uint(part[lane]) : 0u);
+  }
+  float by = 1.f;
+  if (am != 0) {  // (infinities and NaN stay what they are)
+    const int e = am >= 0x80u ? (int)(am >> 7) - 127 : 31 - __clz(am) - 133;  // 2^e <= largest |c| < 2^(e + 1)
+    int k = min(30 - e, 126);
+    if (p.eps > 0.f) k = min(k, (100 - ilogbf(p.eps)) >> 1);
+    by = __uint_as_float((uint32_t)(k + 127) << 23);
+  }
+  float tot = 0.f;
+#pragma unroll 1
+  for (int i = tid; i < nv; i += team) {
+    const uint4 c = current(i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = bf_lo(vword(c, k)) * by, hi = bf_hi(vword(c, k)) * by;
+      tot += lo * lo + hi * hi;
+    }
+  }
+  tot = warp_sum(tot);
+  if constexpr (!WARP_ROWS) {
+    __syncthreads();
+    if (lane == 0) part[warp] = tot;
+    __syncthreads();
+    tot = warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
+  }
+  const float rstd = __frsqrt_rn(tot / p.width + p.eps * by * by);
+  // every lane as long as any has a group (the last scale tile's among them)
+  const int last = (int)(p.q.group_tiles * Mx<FMT>::ATOM_LANES);
+#pragma unroll 1
+  for (int i0 = 0; i0 < last; i0 += team) {
+    const int i = i0 + tid;
+    const uint4 c = current(i);
+    const uint4 w = i < nv ? ld_weight(p.weight + (int64_t)i * 8) : make_uint4(0, 0, 0, 0);
+    f32x2 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      y[k] = f2_mul(f2_mul(f2_mul(bf2_widen(vword(c, k)), f2_make(by, by)), bf2_widen(vword(w, k))),
+                    f2_make(rstd, rstd));
+    norm_store<FMT>(p, t, i, i < nv, y, g, 6.f * g);
+    if (p.delta && i < nv) st_row(prow + (int64_t)i * 8, c);
+  }
+}
+
 template <int FMT, int VPT, int MAX_THREADS, int MIN_CTAS, bool WARP_ROWS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
     attn_res_mx_norm_kernel(const MxNormParams p) {
@@ -205,7 +313,22 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
     tot = warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
   }
   // (the quotient itself: 1 / H as a factor would put its rounding into every row)
-  const float rstd = __frsqrt_rn(tot / p.width + p.eps);
+  const float mean = tot / p.width + p.eps;
+  // (the same in every thread of the row)
+  if (!(mean >= kMxLeastMean && mean < __int_as_float(0x7f800000))) {
+    norm_scaled_row<FMT, WARP_ROWS>(p, t, part);
+    return;
+  }
+  const float rstd = __frsqrt_rn(mean);
+  // The widened elements of the sum are not kept for the products below, where
+  // registers are scarce: kept, 8192 x 7168 took 72.1 us to nvfp4 instead of
+  // 65.4 and 512 x 65536 75.1 to mxfp8 instead of 55.2 (spills); with up to two
+  // vectors a thread and power-of-two scales they are (512 x 4096 to mxfp4 3.03
+  // instead of 3.12).
+  if constexpr (VPT > 2 || M::NV) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) asm("" : "+r"(c[v].x), "+r"(c[v].y), "+r"(c[v].z), "+r"(c[v].w));
+  }
   const f32x2 r2 = f2_make(rstd, rstd);
   uint8_t* const qrow = p.q.data + t * p.q.row_bytes;
   uint8_t* const srow =

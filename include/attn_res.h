@@ -417,7 +417,11 @@ attn_res_status_t attn_res_mx_dequantize(const attn_res_mx_t* q, attn_res_bf16_t
  *   q[t] = y in q's format              (from the fp32 y)
  *
  * the mixture's current row and output norm (as attn_res with no bank rows),
- * its result in the microscaled form.  eps is finite and >= 0.
+ * its result in the microscaled form.  eps is finite and >= 0.  y is held to
+ * fp32 accuracy for rows of any finite magnitude (squares that fp32 does not
+ * hold are taken of the row times a power of two) and weights of up to 2^60
+ * and from 2^-60 on (or 0); a row with an infinity or a NaN, and with eps = 0
+ * a row of zeros, is what the formula makes of it.
  */
 attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
                                    const attn_res_bf16_t* delta, int64_t delta_row,
