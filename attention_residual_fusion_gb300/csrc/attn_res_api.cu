@@ -365,10 +365,10 @@ StreamLaunchFn lookup_stream(int S, int shape, bool d, bool o) {
   }
 }
 
-// Self-test of the bounded waits: one warp waits, with the same code the
-// mixture kernels use and then with that of the microscaled product, on an
-// mbarrier that nothing ever arrives at; every wait must give up after
-// limit_ns, and the stage time-out bit is recorded.
+// Self-test of the bounded waits: three warps wait at once on an mbarrier that
+// nothing ever arrives at, one with the same code as the mixture kernels and
+// two with that of the microscaled product; each must give up after limit_ns,
+// and if all have, the stage time-out bit is recorded.
 __global__ void attn_res_selftest_wait_kernel(unsigned* err, uint64_t limit_ns) {
   __shared__ __align__(8) unsigned long long bar;
   if (threadIdx.x == 0) {
@@ -377,10 +377,11 @@ __global__ void attn_res_selftest_wait_kernel(unsigned* err, uint64_t limit_ns) 
   }
   __syncthreads();
   const uint32_t b = attn_res_dev::smem_addr(&bar);
-  const bool passed = attn_res_dev::mbar_wait_bounded(b, 0u, limit_ns) ||
-                      attn_res_dev::phase_wait<false>(b, 0u, limit_ns) ||
-                      attn_res_dev::phase_wait<true>(b, 0u, limit_ns);
-  if (!passed && threadIdx.x == 0)
+  const int warp = threadIdx.x >> 5;
+  const bool passed = warp == 0   ? attn_res_dev::mbar_wait_bounded(b, 0u, limit_ns)
+                      : warp == 1 ? attn_res_dev::phase_wait<false>(b, 0u, limit_ns)
+                                  : attn_res_dev::phase_wait<true>(b, 0u, limit_ns);
+  if (!__syncthreads_or(passed) && threadIdx.x == 0)
     atomicOr(err, attn_res_dev::kErrStageTimeout);
 }
 
@@ -885,7 +886,7 @@ attn_res_status_t attn_res_selftest_wait_timeout(unsigned int limit_us, unsigned
   cudaError_t e = status_word(dev, &w);
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
   if (e == cudaSuccess) {
-    attn_res_selftest_wait_kernel<<<1, 32, 0, s>>>(w, (uint64_t)limit_us * 1000u);
+    attn_res_selftest_wait_kernel<<<1, 96, 0, s>>>(w, (uint64_t)limit_us * 1000u);
     e = cudaGetLastError();
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess) e = cudaMemcpy(bits, w, sizeof(unsigned), cudaMemcpyDeviceToHost);

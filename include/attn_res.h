@@ -494,10 +494,10 @@ attn_res_status_t attn_res_device_status(unsigned int* bits, int clear);
 
 /*
  * attn_res_selftest_wait_timeout -- exercise the kernels' time-out path on
- * the current device: one warp waits, with each of the bounded waits that
- * the kernels use in turn (three), on an mbarrier that nothing ever completes;
- * after about `limit_us` microseconds (1 .. 1 000 000) a wait gives up, and
- * when all have, bit 0 of the device status word is set.  Synchronous: returns after the kernel
+ * the current device: three warps wait at once, each with one of the bounded
+ * waits that the kernels use, on an mbarrier that nothing ever completes;
+ * after about `limit_us` microseconds (1 .. 1 000 000) they give up, and when
+ * all have, bit 0 of the device status word is set.  Synchronous: returns after the kernel
  * finished, with the status word (not cleared) in *bits.  A diagnostic for
  * tests; it does not touch any caller buffer.
  */

@@ -39,6 +39,16 @@ def test_wait_timeout_is_reported_and_recoverable():
     assert ar.device_status() == 0
 
 
+def test_selftest_takes_one_limit():
+    """All forms of the wait are tried within about one limit."""
+    ar.selftest_wait_timeout(1000)
+    t0 = time.perf_counter()
+    ar.selftest_wait_timeout(200000)  # 200 ms
+    dt = time.perf_counter() - t0
+    assert 0.195 <= dt < 0.35, dt
+    assert ar.device_status(clear=True) & 1
+
+
 def test_selftest_rejects_bad_limits():
     for bad in (0, 2_000_000):
         with pytest.raises(ar.AttnResError):
