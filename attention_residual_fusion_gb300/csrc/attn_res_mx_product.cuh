@@ -242,6 +242,31 @@ struct ProductParams {
   unsigned* err;
 };
 
+// The two tensor scales, for the sums (x * first * second): 1 and their product.
+// Where fp32 does not hold the product (scales of 1e-24 and 1e-20, say, under
+// which a result may well be a number) they are the larger and the smaller:
+// a product below 2^-126 has a larger scale of 2^23 at most, one above 2^128 a
+// smaller of 1 at least, so a sum is out of range between the two
+// multiplications only if the result is.
+struct TensorScales {
+  float first, second;
+};
+template <int FMT>
+__device__ __forceinline__ TensorScales tensor_scales(const ProductParams& p) {
+  const float a = tensor_scale_of(p.a_g), w = tensor_scale_of(p.w_g), both = a * w;
+  if constexpr (FMT != ATTN_RES_NVFP4) return {1.f, both};
+  const bool held = both >= 0x1p-126f && both < __int_as_float(0x7f800000);
+  return {held ? 1.f : fmaxf(a, w), held ? both : fminf(a, w)};
+}
+// (a branch, as 64 more products a thread took 1-3 % of a large product's time)
+template <int N>
+__device__ __forceinline__ void scale_first(const TensorScales& s, uint32_t (&r)[N]) {
+  if (s.first != 1.f) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * s.first);
+  }
+}
+
 // ---- few tokens: weight rows on the instruction's M side, K split over a cluster -----------
 //
 // A CTA makes a part of the sums of 128 output columns (weight rows, the
@@ -352,6 +377,9 @@ __global__ void __launch_bounds__(192, 2)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
+  // (early: read behind the last product, its way from L2 would show)
+  const TensorScales scale = FMT == ATTN_RES_NVFP4 ? tensor_scales<FMT>(p) : TensorScales{1.f, 1.f};
+  const float one = scale.first, by = scale.second;
 
   if (warp == 0 && lane == 0) {
     int issued = ahead;
@@ -390,7 +418,6 @@ __global__ void __launch_bounds__(192, 2)
     if (issuer) mma_commit<1>(done);
     __syncwarp();
   }
-  const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
   if (warp >= 2) {
     // warp w reads the TMEM lanes 32 (w % 4) .., that is the weight rows n0 + those
     const int row = 32 * (warp % 4) + lane;
@@ -409,8 +436,8 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
       for (int j = 0; j < CH; j += 4) {
         if (split == 1) {
-          store_quad(p, m0 + c + j, n0 + row, __uint_as_float(r[j]) * scale, __uint_as_float(r[j + 1]) * scale,
-                     __uint_as_float(r[j + 2]) * scale, __uint_as_float(r[j + 3]) * scale, failed);
+          store_quad(p, m0 + c + j, n0 + row, __uint_as_float(r[j]) * one * by, __uint_as_float(r[j + 1]) * one * by,
+                     __uint_as_float(r[j + 2]) * one * by, __uint_as_float(r[j + 3]) * one * by, failed);
         } else {
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(base + (uint32_t)((c + j) * 32 + row) * 16u),
                        "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3])
@@ -460,8 +487,8 @@ __global__ void __launch_bounds__(192, 2)
             sum.z += part[k][r].z;
             sum.w += part[k][r].w;
           }
-        store_quad(p, m0 + i / 128 * 4, n0 + i % 128, sum.x * scale, sum.y * scale, sum.z * scale, sum.w * scale,
-                   failed);
+        store_quad(p, m0 + i / 128 * 4, n0 + i % 128, sum.x * one * by, sum.y * one * by, sum.z * one * by,
+                   sum.w * one * by, failed);
       }
     }
     // No CTA ends while its part is being read.  Every load's value has been
@@ -726,7 +753,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
     uint32_t tile = 0;
     const int q = warp % 4, part = (warp - 4) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-    const float scale = tensor_scale_of(p.a_g) * tensor_scale_of(p.w_g);
+    const TensorScales scale = tensor_scales<FMT>(p);
     const bool wide = p.out_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     for (int i = first; i < tiles && !failed; i += step, ++tile) {
       int mt, nt;
@@ -754,7 +781,8 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
         tmem_fence_before();
         __syncwarp();
         if ((HALVES == 2 || h == 0) && lane == 0) mbar_arrive_remote(map_rank(acc_empty + 8 * h, 0));
-        pack64(r, scale, v[h]);
+        scale_first(scale, r);
+        pack64(r, scale.second, v[h]);
         if (HALVES == 1 && !failed && row < p.m) store_row64(p, v[h], row, nt * C::TN + local[h], wide);
       }
 #pragma unroll

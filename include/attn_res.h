@@ -433,7 +433,8 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
  * attn_res_mx_matmul -- out[m, n] = sum_k a[m, k] w[n, k], out
  * [a->rows, w->rows] bf16 at out_row, for two matrices of one format and
  * width (a->cols == w->cols); fp32 sums on the tensor cores (tcgen05, block
- * scaled), rounded to bf16 once.  Any number of rows on both sides.
+ * scaled), times the tensor scales, rounded to bf16 once: a result is out of
+ * range only if its value is, whatever the scales.  Any number of rows on both sides.
  * Repeated calls give the same bits.
  *
  * Beside ATTN_RES_FLAG_PDL, flags takes tuning overrides (0 = automatic; the
