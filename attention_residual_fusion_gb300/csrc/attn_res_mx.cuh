@@ -42,8 +42,8 @@ __device__ __forceinline__ bool phase_wait(uint32_t bar, uint32_t parity, uint64
 }
 template <bool PEERS = false>
 __device__ __forceinline__ void phase_or_flag(uint32_t bar, uint32_t parity, bool& failed, unsigned* err,
-                                              unsigned bit) {
-  if (failed || phase_wait<PEERS>(bar, parity)) return;
+                                              unsigned bit, uint64_t limit_ns = kWaitLimitNs) {
+  if (failed || phase_wait<PEERS>(bar, parity, limit_ns)) return;
   failed = true;
   atomicOr(err, bit);
 }

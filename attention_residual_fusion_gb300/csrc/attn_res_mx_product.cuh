@@ -267,6 +267,10 @@ __device__ __forceinline__ void scale_first(const TensorScales& s, uint32_t (&r)
   }
 }
 
+// The limit of a wait for the products of `blocks` blocks of K, each of which
+// takes less than 0.5 us: with the longest rows they take seconds themselves.
+__device__ __forceinline__ uint64_t products_limit_ns(int blocks) { return kWaitLimitNs + 4000ull * (uint32_t)blocks; }
+
 // ---- few tokens: weight rows on the instruction's M side, K split over a cluster -----------
 //
 // A CTA makes a part of the sums of 128 output columns (weight rows, the
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(192, 2)
   if (warp >= 2) {
     // warp w reads the TMEM lanes 32 (w % 4) .., that is the weight rows n0 + those
     const int row = 32 * (warp % 4) + lane;
-    phase_or_flag(done, 0, failed, p.err, kErrStageTimeout);
+    phase_or_flag(done, 0, failed, p.err, kErrStageTimeout, products_limit_ns(blocks));
     failed = __any_sync(0xffffffffu, failed);
     tmem_fence_after();
     grid_dep_launch_dependents();
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (HALVES == 2 || h == 0) {
-          phase_or_flag(acc_full + 8 * h, tile & 1, failed, p.err, kErrStageTimeout);
+          phase_or_flag(acc_full + 8 * h, tile & 1, failed, p.err, kErrStageTimeout, products_limit_ns(blocks));
           failed = __any_sync(0xffffffffu, failed);
           tmem_fence_after();
         }
