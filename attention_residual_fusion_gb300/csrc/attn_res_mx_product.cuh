@@ -271,6 +271,22 @@ __device__ __forceinline__ void scale_first(const TensorScales& s, uint32_t (&r)
 // takes less than 0.5 us: with the longest rows they take seconds themselves.
 __device__ __forceinline__ uint64_t products_limit_ns(int blocks) { return kWaitLimitNs + 4000ull * (uint32_t)blocks; }
 
+// Behind a wait of the issuing warp that has given up at use `use` of stage
+// `stage`: copies under way into the stages land before the CTA ends (bounded
+// again).  A loading thread that has more to issue meets the same end at the
+// stages that are not released, and waits for its own.
+template <int S>
+__device__ __forceinline__ void drain_stages(uint32_t full, int stage, uint32_t use) {
+  uint64_t limit = kWaitLimitNs;
+  for (int k = 0; k < S; ++k) {
+    if (!phase_wait(full + 8 * stage, use & 1, limit)) limit = 0;
+    if (++stage == S) {
+      stage = 0;
+      ++use;
+    }
+  }
+}
+
 // ---- few tokens: weight rows on the instruction's M side, K split over a cluster -----------
 //
 // A CTA makes a part of the sums of 128 output columns (weight rows, the
@@ -405,7 +421,10 @@ __global__ void __launch_bounds__(192, 2)
       const int s = i % S;
       phase_or_flag(full + 8 * s, (i / S) & 1, failed, p.err, kErrStageTimeout);
       failed = __any_sync(0xffffffffu, failed);
-      if (failed) break;
+      if (failed) {
+        drain_stages<S>(full, s, i / S);
+        break;
+      }
       tmem_fence_after();
       if (issuer) {
         const uint32_t sfs = sf_lo + s * (2 * C::SF_BYTES >> 4);
@@ -751,6 +770,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
       if (issuer) mma_commit<2>(drained);
       __syncwarp();
       (void)phase_wait(drained, 0);
+      drain_stages<S>(full, s, use);
     }
   } else if (warp >= 4) {
     bool failed = false;
