@@ -285,7 +285,7 @@ attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t
   const int kernel = static_cast<int>((flags >> 16) & 0xfu), split = static_cast<int>((flags >> 8) & 0xffu);
   if (!scalars_ok(a) || !scalars_ok(w) || a->format != w->format || a->cols != w->cols ||
       !known_flags(flags & ~(ATTN_RES_FLAG_KERNEL(0xf) | ATTN_RES_FLAG_SPLIT(0xff))) ||
-      !product_overrides_ok(*a, kernel, split))
+      !product_overrides_ok(*a, *w, kernel, split))
     return ATTN_RES_EINVAL;
   if (a->rows == 0 || w->rows == 0) return ATTN_RES_OK;
   attn_res_status_t st = check_matrix(*a);

@@ -28,6 +28,6 @@ struct ProductCall {
 };
 cudaError_t launch_mx_product(const ProductCall& c);
 // Whether the overrides can be met.
-bool product_overrides_ok(const attn_res_mx_t& a, int kernel, int split);
+bool product_overrides_ok(const attn_res_mx_t& a, const attn_res_mx_t& w, int kernel, int split);
 
 }  // namespace attn_res_host

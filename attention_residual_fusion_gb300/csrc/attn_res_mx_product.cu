@@ -172,6 +172,9 @@ int64_t wide_cost(const WideCosts& k, const ProductCall& c, int64_t blocks, int 
 
 // Token tiles of the narrow form's grid (its y).
 constexpr int64_t kNarrowMaxRows = int64_t(65535) * 128;
+// Weight rows of the wide forms, whose last tile may reach past them by less
+// than two tiles: their places are 32-bit (of the tensor maps).
+constexpr int64_t kWideMaxColumns = (int64_t(1) << 31) - 2 * 384;
 int64_t k_blocks(const attn_res_mx_t& a) { return (a.cols * mx_bits(a.format) / 8 + 127) / 128; }
 
 // The least cost of the splits 1..kMaxSplit, and that split.
@@ -260,7 +263,9 @@ cudaError_t launch_format(const ProductCall& c) {
   if (kernel == 0) {
     const int64_t one = wide_cost(kWide, c, blocks, 256, one_pairs);
     const int64_t two = wide_cost(kWider, c, blocks, 384, two_pairs);
-    kernel = narrow < (one < two ? one : two) ? ATTN_RES_MX_NARROW : one <= two ? ATTN_RES_MX_WIDE : ATTN_RES_MX_WIDER;
+    kernel = narrow < (one < two ? one : two) || c.w->rows > kWideMaxColumns ? ATTN_RES_MX_NARROW
+             : one <= two                                                    ? ATTN_RES_MX_WIDE
+                                                                             : ATTN_RES_MX_WIDER;
   }
   if (kernel == ATTN_RES_MX_WIDE) return One::launch(c, one_pairs);
   if (kernel == ATTN_RES_MX_WIDER) return Two::launch(c, two_pairs);
@@ -283,10 +288,10 @@ cudaError_t launch_mx_product(const ProductCall& c) {
   }
 }
 
-bool product_overrides_ok(const attn_res_mx_t& a, int kernel, int split) {
+bool product_overrides_ok(const attn_res_mx_t& a, const attn_res_mx_t& w, int kernel, int split) {
   if (kernel < 0 || kernel > ATTN_RES_MX_WIDER) return false;
   if (kernel == ATTN_RES_MX_NARROW) return a.rows <= kNarrowMaxRows && split <= kMaxSplit && split <= k_blocks(a);
-  return split == 0;
+  return split == 0 && (kernel == 0 || w.rows <= kWideMaxColumns);
 }
 
 }  // namespace attn_res_host

@@ -442,7 +442,8 @@ attn_res_status_t attn_res_mx_norm(attn_res_bf16_t* prefix, int64_t prefix_row,
  *   KERNEL(k): ATTN_RES_MX_NARROW -- a CTA for 128 rows of w and up to 128 of
  *              a, K split over a cluster (few tokens, or few tiles);
  *              ATTN_RES_MX_WIDE, ATTN_RES_MX_WIDER -- persistent CTA pairs,
- *              256 rows of a and 256 or 384 of w at a time;
+ *              256 rows of a and 256 or 384 of w at a time (w->rows up to
+ *              2^31 - 768);
  *   SPLIT(s):  with ATTN_RES_MX_NARROW, the CTAs that share a tile's K: 1..6,
  *              at most the 128-byte blocks of a row of codes.
  * An override that cannot be met is ATTN_RES_EINVAL.

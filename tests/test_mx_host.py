@@ -210,3 +210,18 @@ def test_binding_refuses_what_is_not_on_the_gpu(lib):
         mx.MxTensor.empty(4, 64, "mxfp6")
     with pytest.raises(ValueError):
         mx.MxTensor.empty(4, 48, "mxfp4")
+
+
+def test_wide_forms_take_columns_up_to_their_32_bit_places(lib):
+    """A tile that reaches past the last column stays below 2^31."""
+    def status(n, kernel):
+        w = matrix(2, fmt=2, rows=n, cols=32, row_bytes=16, scales=addr(9))
+        return matmul(a=matrix(1, rows=1, cols=32, row_bytes=16), w=w, out_row=(n + 7) // 8 * 8,
+                      flags=ar.FLAG_KERNEL(kernel))
+    largest = (1 << 31) - 256
+    for kernel in (2, 3):
+        assert status(largest, kernel) == 1
+        assert status((1 << 31) - 767, kernel) == 1
+    if not torch.cuda.is_available():
+        assert all(status(largest, k) in (4, 5) for k in (0, 1))
+        assert all(status((1 << 31) - 768, k) in (4, 5) for k in (2, 3))
