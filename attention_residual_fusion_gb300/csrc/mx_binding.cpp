@@ -147,6 +147,8 @@ struct On {
       device.set_device(d);
       handle = c10::cuda::getCurrentCUDAStream(d.index()).stream();
     } else {
+      if (!py::hasattr(s, "stream_id") || !py::hasattr(s, "device_index") || !py::hasattr(s, "device_type"))
+        refuse("stream must be a torch.cuda.Stream");
       const auto given = c10::cuda::CUDAStream::unpack3(
           s.attr("stream_id").cast<int64_t>(), static_cast<c10::DeviceIndex>(s.attr("device_index").cast<int64_t>()),
           static_cast<c10::DeviceType>(s.attr("device_type").cast<int64_t>()));
@@ -175,6 +177,7 @@ py::object result(const py::object& out, int64_t rows, int64_t cols, const std::
     *c = made.cast<const MxTensor&>().matrix();
     return made;
   }
+  if (!py::isinstance<MxTensor>(out)) refuse("out must be an MxTensor");
   const MxTensor& o = out.cast<const MxTensor&>();
   if (o.format != f || (g && !(o.global_scale && g->is_same(*o.global_scale))))
     refuse("out has another format or global_scale");

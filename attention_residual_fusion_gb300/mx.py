@@ -17,7 +17,8 @@ Each call takes ``stream``: the stream that it runs on, as torch.cuda.stream
 would set it (outputs are allocated there too); the current one by default.
 Tensors on another device than the current one run there.  ``pdl`` is
 programmatic dependent launch (see ATTN_RES_FLAG_PDL and the notes on the
-microscaled calls).  Arguments that cannot be marshalled raise ValueError,
+microscaled calls).  Arguments that cannot be marshalled raise ValueError (or
+TypeError where another type was given for a tensor, a matrix or a number),
 those that the library refuses AttnResError.
 """
 from __future__ import annotations

@@ -139,3 +139,24 @@ def test_parts_that_no_longer_fit():
         for call in (lambda: mx.matmul(x, a), lambda: mx.matmul(a, x), lambda: mx.dequantize(a)):
             with pytest.raises(ValueError):
                 call()
+
+
+def test_wrong_types():
+    """What is no matrix, no stream or no tensor is refused as documented."""
+    x = activations(4, 64, 1)
+    one = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    q = mx.quantize(x, "mxfp8")
+    for bad in (x, "q", 3, q.data):
+        with pytest.raises(ValueError, match="out"):
+            mx.quantize(x, "mxfp8", out=bad)
+        with pytest.raises(ValueError, match="out"):
+            mx.add_rms_norm(x, None, one, out=bad)
+    for bad in ("s", 0, x, torch.cuda.current_stream().cuda_stream):
+        with pytest.raises(ValueError, match="stream"):
+            mx.matmul(q, q, stream=bad)
+        with pytest.raises(ValueError, match="stream"):
+            mx.dequantize(q, stream=bad)
+    for call in (lambda: mx.dequantize(x), lambda: mx.matmul(q, x), lambda: mx.quantize(q), lambda: mx.quantize(x, 3)):
+        with pytest.raises(TypeError):
+            call()
+    assert torch.equal(mx.matmul(q, q, stream=torch.cuda.current_stream()), mx.matmul(q, q))
