@@ -26,6 +26,7 @@ from __future__ import annotations
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 from . import _build, lib
 
@@ -34,6 +35,7 @@ GROUP = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 # Forms of the product (matmul's kernel=; 0: automatic), see attn_res_mx_matmul.
 KERNEL_NARROW, KERNEL_WIDE, KERNEL_WIDER = 1, 2, 3
 _CALLS = ("MxTensor", "quantize", "dequantize", "add_rms_norm", "matmul")
+_loading = threading.Lock()
 
 
 def scales_shape(format: str, rows: int, cols: int) -> tuple:
@@ -60,5 +62,7 @@ def _load():
 def __getattr__(name: str):
     if name not in _CALLS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    _load()
+    with _loading:  # a second thread's load would find the module half made
+        if name not in globals():
+            _load()
     return globals()[name]

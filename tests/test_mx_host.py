@@ -2,6 +2,9 @@
 hand-worked values, the scale layout, and every refusal (validation precedes
 the first CUDA call, so no GPU is needed)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -225,3 +228,33 @@ def test_wide_forms_take_columns_up_to_their_32_bit_places(lib):
     if not torch.cuda.is_available():
         assert all(status(largest, k) in (4, 5) for k in (0, 1))
         assert all(status((1 << 31) - 768, k) in (4, 5) for k in (2, 3))
+
+
+THREADS = r"""
+import sys
+import threading
+import torch
+from attention_residual_fusion_gb300 import mx
+sys.setswitchinterval(1e-6)
+start, got, errors = threading.Barrier(16), [], []
+def first():
+    start.wait()
+    try:
+        got.append((mx.MxTensor, mx.matmul))
+    except BaseException as e:
+        errors.append(repr(e))
+threads = [threading.Thread(target=first) for _ in range(16)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+assert not errors, errors
+assert len(got) == 16 and len(set(got)) == 1
+"""
+
+
+def test_first_use_from_many_threads(lib):
+    """The binding is loaded once, whichever of the threads come first."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", THREADS], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
