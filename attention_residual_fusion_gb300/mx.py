@@ -30,7 +30,6 @@ import threading
 
 from . import _build, lib
 
-FORMATS = {"mxfp8": 1, "mxfp4": 2, "nvfp4": 3}
 GROUP = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 # Forms of the product (matmul's kernel=; 0: automatic), see attn_res_mx_matmul.
 KERNEL_NARROW, KERNEL_WIDE, KERNEL_WIDER = 1, 2, 3
