@@ -52,11 +52,19 @@ int64_t row_stride(const at::Tensor& t, int64_t to) {
 // The address of a tensor's first element.  A storage can shrink under its
 // tensors (untyped_storage().resize_()): elements outside it have no address.
 void* address(const char* name, const at::Tensor& t) {
-  if (t.numel() == 0) return t.data_ptr();
-  int64_t last = t.storage_offset();
-  for (int64_t d = 0; d < t.dim(); ++d) last += (t.size(d) - 1) * t.stride(d);
-  if ((static_cast<size_t>(last) + 1) * t.element_size() > t.storage().nbytes())
-    refuse(std::string(name) + "'s storage does not hold its elements");
+  const c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  const int64_t n = impl->numel();
+  if (n > 0) {
+    int64_t last = impl->storage_offset();
+    if (impl->is_contiguous()) {
+      last += n - 1;
+    } else {
+      const at::IntArrayRef size = impl->sizes(), stride = impl->strides();
+      for (size_t d = 0; d < size.size(); ++d) last += (size[d] - 1) * stride[d];
+    }
+    if ((static_cast<size_t>(last) + 1) * impl->itemsize() > impl->unsafe_storage().nbytes())
+      refuse(std::string(name) + "'s storage does not hold its elements");
+  }
   return t.data_ptr();
 }
 
@@ -73,13 +81,14 @@ struct MxTensor {
   OptTensor global_scale;
   int format;
 
-  int64_t rows() const { return data.size(0); }
-  int64_t cols() const { return data.size(1) * (format == ATTN_RES_MXFP8 ? 1 : 2); }
+  int64_t rows() const { return data.sizes().at(0); }
+  int64_t cols() const { return data.sizes().at(1) * (format == ATTN_RES_MXFP8 ? 1 : 2); }
   at::Device device() const { return data.device(); }
 
   void check() const {
-    if (data.scalar_type() != data_type(format) || data.dim() != 2 || !data.is_cuda() ||
-        (data.stride(1) != 1 && data.size(1) > 1))
+    const at::IntArrayRef size = data.sizes();
+    if (data.scalar_type() != data_type(format) || size.size() != 2 || !data.is_cuda() ||
+        (data.strides()[1] != 1 && size[1] > 1))
       refuse(std::string("data must be a CUDA ") + c10::toString(data_type(format)) +
              " matrix with unit inner stride");
     const auto shape = scales_shape(format, rows(), cols());
