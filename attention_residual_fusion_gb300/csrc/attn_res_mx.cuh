@@ -130,10 +130,12 @@ __device__ __forceinline__ GroupScale<FMT> group_scale(uint32_t amax, float g, f
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): 3 instructions a pair in place of two divisions.  Nothing
 // over- or underflows on the way that matters: the divisor is between 2^-96
-// and 2^96, the quotient at most 7 (the group's scale is not saturated), and
+// and 2^96, the quotient below 9 (the group's scale is not saturated: 6 times
+// what its rounding takes off, 17/16 at most for a normal e4m3 scale and below
+// 1.5 for the subnormal ones; the conversion saturates what is above 6), and
 // where x is so small that its remainder is lost, the quotient is far below
-// half the smallest code.  Negated, because so a zero keeps its
-// sign (0 - 0 is +0 only in the remainder).
+// half the smallest code.  Negated, because so a zero keeps its sign (0 - 0 is
+// +0 only in the remainder).
 __device__ __forceinline__ f32x2 negated_quotient2(f32x2 x, float by, float inverse) {
   const f32x2 r = f2_make(-inverse, -inverse);
   const f32x2 q = f2_mul(x, r);

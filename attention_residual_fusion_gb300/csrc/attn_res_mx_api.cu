@@ -188,7 +188,7 @@ NormShape norm_shape(int format, int64_t nv, int64_t rows) {
 // The many-row shapes in the other formats: 8192 x 7168 59.5 us to mxfp4 and
 // 64.9 to nvfp4 (16 bytes of spills a thread).  Above 32768 columns 1024
 // threads of 64 registers spill about 150 bytes each: 512 x 65536 to mxfp8
-// 55.2 us, for 45.7 us of bytes.
+// 55.2 us, for 34.7 us of bytes.
 constexpr int64_t kNormManyRows = 1024;
 NormShape norm_shape(int format, int64_t nv, int64_t rows) {
   if (rows >= kNormManyRows) {
