@@ -255,8 +255,9 @@ template <int FMT>
 __device__ __forceinline__ TensorScales tensor_scales(const ProductParams& p) {
   const float a = tensor_scale_of(p.a_g), w = tensor_scale_of(p.w_g), both = a * w;
   if constexpr (FMT != ATTN_RES_NVFP4) return {1.f, both};
-  const bool held = both >= 0x1p-126f && both < __int_as_float(0x7f800000);
-  return {held ? 1.f : fmaxf(a, w), held ? both : fminf(a, w)};
+  const bool held = fabsf(both) >= 0x1p-126f && fabsf(both) < __int_as_float(0x7f800000);
+  const bool w_larger = fabsf(a) < fabsf(w);  // (not fmaxf and fminf: a NaN stays one)
+  return {held ? 1.f : w_larger ? w : a, held ? both : w_larger ? a : w};
 }
 // (a branch, as 64 more products a thread took 1-3 % of a large product's time)
 template <int N>

@@ -83,3 +83,24 @@ def test_results_out_of_range():
         assert (mx.matmul(small.t, small.t, **kw) == 0).all()
         assert torch.isfinite(mx.matmul(big.t, one.t, **kw)).all()
         check(mx.matmul(big.t, small.t, **kw), matrix_values(big, 1e30), matrix_values(small, 1e-30), 64)
+
+
+@pytest.mark.parametrize("M", [3, 60, 200])
+def test_scales_that_are_no_numbers(M):
+    """A tensor scale of NaN makes every result NaN, on either side; a negative one negates."""
+    N, K = 130, 288
+    rng = np.random.default_rng(9)
+    a, w = (R.quantize(rng.standard_normal((r, K)), "nvfp4", 1.0) for r in (M, N))
+
+    def at(codes, rows, g):
+        return Matrix(rows, K, "nvfp4", 0, torch.tensor([g], device="cuda")).set(*codes).t
+    for name in FORMS:
+        kw = form(name, "nvfp4", K)
+        for ga, gw in ((float("nan"), 0.5), (0.5, float("nan")), (float("nan"), float("nan"))):
+            assert torch.isnan(mx.matmul(at(a, M, ga), at(w, N, gw), **kw)).all(), name
+        want = mx.matmul(at(a, M, 0.5), at(w, N, 0.25), **kw)
+        assert torch.equal(mx.matmul(at(a, M, -0.5), at(w, N, 0.25), **kw), -want), name
+        far = mx.matmul(at(a, M, 1e30), at(w, N, 1e6), **kw)
+        assert torch.equal(mx.matmul(at(a, M, 1e30), at(w, N, -1e6), **kw), -far), name
+        tiny = mx.matmul(at(a, M, 1e-30), at(w, N, 1e-9), **kw)
+        assert torch.equal(mx.matmul(at(a, M, -1e-30), at(w, N, 1e-9), **kw), -tiny) and bool((tiny != 0).any()), name
