@@ -342,9 +342,10 @@ def _exact_act(g, act):
     if act == "silu":
         p = torch.sigmoid(g)
         return g * p, p * (1 + g * (1 - p))
-    k = math.sqrt(2 / math.pi)
-    t = torch.tanh(k * (g + 0.044715 * g ** 3))
-    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g)
+    # (1 + tanh(y)) / 2 as the sigmoid of 2 y: 1 + tanh loses all of small values
+    k = math.sqrt(8 / math.pi)
+    p = torch.sigmoid(k * (g + 0.044715 * g ** 3))
+    return g * p, p + g * p * (1 - p) * k * (1 + 3 * 0.044715 * g * g)
 
 
 def exact(case, seed):
