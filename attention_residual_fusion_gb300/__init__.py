@@ -54,7 +54,9 @@ EXPORTS = ("attn_res", "attn_res_status_string", "attn_res_hidden_size",
            "attn_res_selftest_wait_timeout", "attn_res_h", "attn_res_tp_sums",
            "attn_res_tp_sq", "attn_res_tp_finish", "attn_res_tp_sums_width",
            "attn_res_mx_scale_bytes", "attn_res_mx_quantize", "attn_res_mx_dequantize",
-           "attn_res_mx_norm", "attn_res_mx_matmul")
+           "attn_res_mx_norm", "attn_res_mx_matmul", "attn_res_f8_quantize",
+           "attn_res_f8_dequantize", "attn_res_f8_matmul", "attn_res_f8_gated",
+           "attn_res_f8_gated_backward")
 
 
 class Layout(ctypes.Structure):
@@ -70,6 +72,13 @@ class Mx(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
                 ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p)]
+
+
+class F8(ctypes.Structure):
+    """attn_res_f8_t"""
+    _fields_ = [("block", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scales_row", ctypes.c_int64)]
 
 
 class AttnResError(RuntimeError):
@@ -138,8 +147,38 @@ def lib():
         L.attn_res_mx_norm.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, mp, u32, vp]
         L.attn_res_mx_matmul.restype = ctypes.c_int
         L.attn_res_mx_matmul.argtypes = [mp, mp, vp, i64, u32, vp]
+        fp = ctypes.POINTER(F8)
+        L.attn_res_f8_quantize.restype = ctypes.c_int
+        L.attn_res_f8_quantize.argtypes = [vp, i64, fp, fp, u32, vp]
+        L.attn_res_f8_dequantize.restype = ctypes.c_int
+        L.attn_res_f8_dequantize.argtypes = [fp, vp, i64, u32, vp]
+        L.attn_res_f8_matmul.restype = ctypes.c_int
+        L.attn_res_f8_matmul.argtypes = [fp, fp, fp, fp, vp, i64, i32, u32, vp]
+        L.attn_res_f8_gated.restype = ctypes.c_int
+        L.attn_res_f8_gated.argtypes = [fp, fp, fp, i32, fp, vp, i64, fp, fp, u32, vp]
+        L.attn_res_f8_gated_backward.restype = ctypes.c_int
+        L.attn_res_f8_gated_backward.argtypes = [vp, i64, fp, fp, i32, fp, fp, fp, fp, fp, u32, vp]
         _lib = L
     return _lib
+
+
+def load_binding(name: str, path: str, calls) -> dict:
+    """The calls of a compiled binding of the library's entry points."""
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (the binding's libraries)
+
+    lib()
+    if not os.path.exists(path):
+        raise RuntimeError(
+            f"{path} is missing: build it with "
+            "attention_residual_fusion_gb300._build.build() (or __graft_entry__.build())")
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    spec = importlib.util.spec_from_file_location(name, path, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    return {c: getattr(module, c) for c in calls}
 
 
 def status_string(status: int) -> str:

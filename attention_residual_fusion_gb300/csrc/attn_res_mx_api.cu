@@ -4,6 +4,7 @@
 // is written unless every check passes.
 #include <cmath>
 
+#include "attn_res_checks.cuh"
 #include "attn_res_mx_host.cuh"
 #include "attn_res_mx_rows.cuh"
 
@@ -14,35 +15,9 @@ using namespace attn_res_host;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;  // tensor-map coordinates and grids are 32-bit
 constexpr int64_t kMaxCols = int64_t(1) << 30;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int64_t kMaxNormCols = 8 * 8 * kMxNormMaxThreads;
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// A byte range an argument covers.
-struct Span {
-  uintptr_t lo = 0, hi = 0;
-  bool written = false;
-};
-Span span(const void* p, int64_t bytes, bool written) {
-  Span s;
-  if (p != nullptr) {
-    s.lo = reinterpret_cast<uintptr_t>(p);
-    s.hi = s.lo + static_cast<uintptr_t>(bytes);
-  }
-  s.written = written;
-  return s;
-}
-template <int N>
-bool written_overlap(const Span (&s)[N]) {
-  for (int i = 0; i < N; ++i)
-    for (int j = 0; j < N; ++j)
-      if (i != j && s[i].written && s[i].lo < s[j].hi && s[j].lo < s[i].hi) return true;
-  return false;
-}
-
 bool known_format(int f) { return f == ATTN_RES_MXFP8 || f == ATTN_RES_MXFP4 || f == ATTN_RES_NVFP4; }
-bool known_flags(uint32_t f) { return (f & ~ATTN_RES_FLAG_PDL) == 0; }
 int64_t code_bytes(const attn_res_mx_t& q) { return q.cols * mx_bits(q.format) / 8; }
 int64_t scale_bytes(const attn_res_mx_t& q) {
   return (q.rows + 127) / 128 * mx_group_tiles(q.format, q.cols) * 512;
@@ -54,9 +29,6 @@ bool scalars_ok(const attn_res_mx_t* q) {
          q->cols <= kMaxCols && q->cols % 32 == 0 &&
          (q->tensor_scale == nullptr || q->format == ATTN_RES_NVFP4);
 }
-// (rows - 1) * stride below 2^60: extents in bytes stay far from overflow.
-bool span_ok(int64_t rows, int64_t stride) { return rows <= 1 || stride <= (int64_t(1) << 60) / (rows - 1); }
-
 attn_res_status_t check_matrix(const attn_res_mx_t& q) {
   if (!q.data || !q.scales || q.row_bytes < code_bytes(q) || q.row_bytes >= kMaxStride ||
       !span_ok(q.rows, q.row_bytes))
@@ -65,15 +37,6 @@ attn_res_status_t check_matrix(const attn_res_mx_t& q) {
       !aligned(q.tensor_scale, 4))
     return ATTN_RES_EALIGN;
   return ATTN_RES_OK;
-}
-// bf16 rows; `width` columns are used.
-attn_res_status_t check_rows(const attn_res_bf16_t* x, int64_t rows, int64_t row, int64_t width) {
-  if (!x || row < width || row > kMaxStride || !span_ok(rows, row)) return ATTN_RES_EINVAL;
-  if (!aligned(x, 16) || row % 8 != 0) return ATTN_RES_EALIGN;
-  return ATTN_RES_OK;
-}
-Span rows_span(const attn_res_bf16_t* x, int64_t rows, int64_t row, int64_t width, bool written) {
-  return span(x, ((rows - 1) * row + width) * 2, written);
 }
 Span data_span(const attn_res_mx_t& q, bool written) {
   return span(q.data, (q.rows - 1) * q.row_bytes + code_bytes(q), written);
@@ -92,30 +55,6 @@ MxView view(const attn_res_mx_t& q) {
   v.group_tiles = mx_group_tiles(q.format, q.cols);
   return v;
 }
-
-attn_res_status_t launched(cudaError_t e) {
-  if (e == cudaSuccess) return ATTN_RES_OK;
-  (void)cudaGetLastError();
-  return ATTN_RES_ECUDA;
-}
-
-// A programmatic launch: the kernel's start-up overlaps the end of a preceding
-// kernel that lets its dependents start, and it waits for that kernel before
-// it touches memory.
-struct Launch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  Launch(int64_t grid, int threads, void* stream) {
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-  }
-  Launch(const Launch&) = delete;
-};
 
 // Both directions of the conversion share their checks and their grid.
 template <class Kern>

@@ -3,15 +3,11 @@
 
 #include <cuda_runtime.h>
 
+#include "attn_res_checks.cuh"
 #include "attn_res_launch.cuh"
 #include "attn_res_mx_product.cuh"
 
 namespace attn_res_host {
-
-// Defined in attn_res_api.cu: the current device, if it is one the kernels
-// run on, and its status word.
-attn_res_status_t current_device(int* device);
-cudaError_t device_status_word(int device, unsigned** word);
 
 // Defined in attn_res_mx_product.cu: the launch of a checked product.
 struct ProductCall {

@@ -1,30 +1,11 @@
 // attn_res_mx_product.cu -- launches of the microscaled product.
 #include "attn_res_mx_host.cuh"
+#include "attn_res_tensor_host.cuh"
 
 namespace attn_res_host {
 namespace {
 
 using namespace attn_res_dev;
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encode_tiled(EncodeTiled* out) {
-  static std::atomic<void*> found{nullptr};
-  void* f = found.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    cudaDriverEntryPointQueryResult state;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                     cudaEnableDefault, &state);
-    if (e != cudaSuccess) return e;
-    if (state != cudaDriverEntryPointSuccess || f == nullptr) return cudaErrorNotSupported;
-    found.store(f, std::memory_order_release);
-  }
-  *out = reinterpret_cast<EncodeTiled>(f);
-  return cudaSuccess;
-}
 
 // Tensor map of an operand's codes as bytes: boxes of 128 bytes x `rows`,
 // 128-byte swizzle; bytes past the row's end and rows past the last read as 0.
@@ -74,18 +55,6 @@ ProductParams params(const ProductCall& c) {
   p.early_weights = c.pdl;
   p.err = c.err;
   return p;
-}
-
-// The dynamic shared memory above 48 KB is opt-in, per function and device.
-template <class Kern>
-cudaError_t allow_smem(Kern kern, uint32_t bytes, int device, std::atomic<uint64_t>& enabled) {
-  const uint64_t bit = 1ull << device;
-  if (!(enabled.load(std::memory_order_acquire) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    enabled.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  return cudaSuccess;
 }
 
 // Every launch is a programmatic one: its start-up overlaps the end of a

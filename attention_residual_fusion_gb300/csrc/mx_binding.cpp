@@ -3,26 +3,11 @@
 // ctypes binding's, compiled because a decode step's calls take the GPU two to
 // six microseconds each and interpreted marshalling with two allocations took
 // fourteen.  PyTorch provides the device memory, the streams and the tensors.
-#include <ATen/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <pybind11/stl.h>
-#include <torch/csrc/utils/pybind.h>
-
-#include <optional>
-#include <string>
-#include <tuple>
-
-#include "attn_res.h"
-
-namespace py = pybind11;
+#include "binding.h"
 
 namespace {
 
-using OptTensor = std::optional<at::Tensor>;
-
-[[noreturn]] void refuse(const std::string& why) { throw py::value_error(why); }
+using namespace attn_res_binding;
 
 int format_code(const std::string& f) {
   if (f == "mxfp8") return ATTN_RES_MXFP8;
@@ -37,35 +22,6 @@ at::ScalarType data_type(int f) { return f == ATTN_RES_MXFP8 ? at::kFloat8_e4m3f
 at::ScalarType scales_type(int f) { return f == ATTN_RES_NVFP4 ? at::kFloat8_e4m3fn : at::kFloat8_e8m0fnu; }
 std::array<int64_t, 5> scales_shape(int f, int64_t rows, int64_t cols) {
   return {(rows + 127) / 128, (cols / (f == ATTN_RES_NVFP4 ? 16 : 32) + 3) / 4, 32, 4, 4};
-}
-
-at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType type, at::Device device) {
-  return at::detail::empty_cuda(shape, type, device, std::nullopt);
-}
-
-// The stride of a single row says nothing (it may be anything): such a matrix
-// gets the least that the entry points take.
-int64_t row_stride(const at::Tensor& t, int64_t to) {
-  return t.size(0) > 1 ? t.stride(0) : (t.size(1) + to - 1) / to * to;
-}
-
-// The address of a tensor's first element.  A storage can shrink under its
-// tensors (untyped_storage().resize_()): elements outside it have no address.
-void* address(const char* name, const at::Tensor& t) {
-  const c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
-  const int64_t n = impl->numel();
-  if (n > 0) {
-    int64_t last = impl->storage_offset();
-    if (impl->is_contiguous()) {
-      last += n - 1;
-    } else {
-      const at::IntArrayRef size = impl->sizes(), stride = impl->strides();
-      for (size_t d = 0; d < size.size(); ++d) last += (size[d] - 1) * stride[d];
-    }
-    if ((static_cast<size_t>(last) + 1) * impl->itemsize() > impl->unsafe_storage().nbytes())
-      refuse(std::string(name) + "'s storage does not hold its elements");
-  }
-  return t.data_ptr();
 }
 
 void check_global_scale(int f, const OptTensor& g, at::Device device) {
@@ -129,53 +85,6 @@ MxTensor allocate(int64_t rows, int64_t cols, int f, const OptTensor& g, at::Dev
   return {new_tensor({rows, f == ATTN_RES_MXFP8 ? cols : cols / 2}, data_type(f), device),
           new_tensor(scales_shape(f, rows, cols), scales_type(f), device), g, f};
 }
-
-void check_rows(const char* name, const at::Tensor& t) {
-  if (t.scalar_type() != at::kBFloat16 || !t.is_cuda()) refuse(std::string(name) + " must be a CUDA bfloat16 tensor");
-  if (t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
-    refuse(std::string(name) + " must be a 2-D matrix with unit inner stride");
-}
-void check_rows(const char* name, const at::Tensor& t, int64_t rows, int64_t cols, at::Device device) {
-  check_rows(name, t);
-  if (t.size(0) != rows || t.size(1) != cols)
-    refuse(std::string(name) + " must be a [" + std::to_string(rows) + ", " + std::to_string(cols) + "] matrix");
-  if (t.device() != device) refuse("all tensors of a call must be on one device");
-}
-attn_res_bf16_t* bf16(const char* name, const at::Tensor& t) {
-  return static_cast<attn_res_bf16_t*>(address(name, t));
-}
-
-// The device and stream of a call: current while outputs are allocated and the
-// kernel is launched.
-struct On {
-  c10::cuda::OptionalCUDAGuard device;
-  c10::cuda::OptionalCUDAStreamGuard stream;
-  void* handle;
-  On(at::Device d, const py::object& s) {
-    if (s.is_none()) {
-      device.set_device(d);
-      handle = c10::cuda::getCurrentCUDAStream(d.index()).stream();
-    } else {
-      if (!py::hasattr(s, "stream_id") || !py::hasattr(s, "device_index") || !py::hasattr(s, "device_type"))
-        refuse("stream must be a torch.cuda.Stream");
-      const auto given = c10::cuda::CUDAStream::unpack3(
-          s.attr("stream_id").cast<int64_t>(), static_cast<c10::DeviceIndex>(s.attr("device_index").cast<int64_t>()),
-          static_cast<c10::DeviceType>(s.attr("device_type").cast<int64_t>()));
-      if (given.device() != d) refuse("stream must belong to the tensors' device");
-      stream.reset_stream(given);
-      handle = given.stream();
-    }
-  }
-};
-
-void check(attn_res_status_t st) {
-  if (st == ATTN_RES_OK) return;
-  const py::object type = py::module_::import("attention_residual_fusion_gb300").attr("AttnResError");
-  const py::object error = type(static_cast<int>(st), attn_res_status_string(st));
-  PyErr_SetObject(type.ptr(), error.ptr());
-  throw py::error_already_set();
-}
-uint32_t flags_of(bool pdl) { return pdl ? ATTN_RES_FLAG_PDL : 0u; }
 
 // The result of a quantising call: `out`, checked, or a new one.
 py::object result(const py::object& out, int64_t rows, int64_t cols, const std::string& format, const OptTensor& g,

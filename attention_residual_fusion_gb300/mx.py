@@ -23,12 +23,9 @@ those that the library refuses AttnResError.
 """
 from __future__ import annotations
 
-import importlib.machinery
-import importlib.util
-import os
 import threading
 
-from . import _build, lib
+from . import _build, load_binding
 
 GROUP = {"mxfp8": 32, "mxfp4": 32, "nvfp4": 16}
 # Forms of the product (matmul's kernel=; 0: automatic), see attn_res_mx_matmul.
@@ -43,25 +40,10 @@ def scales_shape(format: str, rows: int, cols: int) -> tuple:
     return ((rows + 127) // 128, (cols // GROUP[format] + 3) // 4, 32, 4, 4)
 
 
-def _load():
-    import torch  # noqa: F401  (the binding's libraries)
-
-    lib()
-    if not os.path.exists(_build.BINDING):
-        raise RuntimeError(
-            f"{_build.BINDING} is missing: build it with "
-            "attention_residual_fusion_gb300._build.build() (or __graft_entry__.build())")
-    loader = importlib.machinery.ExtensionFileLoader("_mx", _build.BINDING)
-    spec = importlib.util.spec_from_file_location("_mx", _build.BINDING, loader=loader)
-    module = importlib.util.module_from_spec(spec)
-    loader.exec_module(module)
-    globals().update({name: getattr(module, name) for name in _CALLS})
-
-
 def __getattr__(name: str):
     if name not in _CALLS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     with _loading:  # a second thread's load would find the module half made
         if name not in globals():
-            _load()
+            globals().update(load_binding("_mx", _build.BINDING, _CALLS))
     return globals()[name]

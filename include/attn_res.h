@@ -455,6 +455,126 @@ attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t
                                      attn_res_bf16_t* out, int64_t out_row, uint32_t flags,
                                      void* stream);
 
+/*
+ * Rows in 8 bits with scales for blocks of 128: e4m3 elements, an fp32 scale for
+ * 128 of them along a row (activations and gradients) or for a block of 128 x
+ * 128 (weights), the form in which a feed-forward block is run and trained in 8
+ * bits.  The calls below bring rows into it, also transposed, multiply two such
+ * matrices, and make the gated block's first half and its backward pass.  (No
+ * counterpart on the pages.)
+ *
+ * An element of a group with scale s stands for code * s.  Quantisation, with
+ * amax the group's largest |x|:
+ *   s = max(amax / 448, 2^-126), 1 for a group of zeros;
+ *   code = rn_e4m3(x / s), saturating at +-448
+ * (fp32 quotients, correctly rounded; rn: to nearest, ties to even).  A group
+ * that holds a NaN or an infinity gets the scale NaN and zero codes: it stands
+ * for NaN throughout.  Scales that a caller makes may be any fp32 values.
+ *
+ * Data: element k of row r is the byte data[r * row_bytes + k].  Any number of
+ * columns; data 16-byte aligned and row_bytes a multiple of 16 (for one row: at
+ * least cols).  Bytes past a row's last are neither read nor written.
+ * Scales, with b = k / 128:
+ *   ATTN_RES_F8_ROWS    scales[b * scales_row + r]: blocks of columns outermost,
+ *                       scales_row >= rows and a multiple of 4, 16-byte aligned;
+ *   ATTN_RES_F8_SQUARE  scales[(r / 128) * scales_row + b], scales_row >= the
+ *                       blocks of a row, 4-byte aligned.
+ * Floats between the last of a row of scales and the next row are neither read
+ * nor written.  A matrix without elements (rows or cols 0) may have null
+ * pointers.
+ */
+#define ATTN_RES_F8_ROWS 1
+#define ATTN_RES_F8_SQUARE 128
+
+typedef struct {
+  int32_t block;       /* ATTN_RES_F8_ROWS or ATTN_RES_F8_SQUARE */
+  int64_t rows, cols;  /* 0 .. 2^31 - 1024 each */
+  void* data;          /* e4m3 codes */
+  int64_t row_bytes;   /* between rows of data */
+  float* scales;
+  int64_t scales_row;  /* floats between rows of scales */
+} attn_res_f8_t;
+
+/* Enqueueing, flags, alignment of bf16 rows, aliasing and errors are as for the
+ * microscaled calls above; all outputs of a call are disjoint from each other
+ * and from its inputs.  Where nothing is to be written, a call checks the scalar
+ * arguments and returns OK. */
+
+/* q = x [q->rows, q->cols], and, if qt is not NULL, qt = the transposed x
+ * [q->cols, q->rows], quantised by itself: with ATTN_RES_F8_ROWS in groups along
+ * the columns of x.  Both have one kind of block. */
+attn_res_status_t attn_res_f8_quantize(const attn_res_bf16_t* x, int64_t x_row,
+                                       const attn_res_f8_t* q, const attn_res_f8_t* qt,
+                                       uint32_t flags, void* stream);
+
+/* x = the bf16 values that q stands for (code * s in fp32, rounded once). */
+attn_res_status_t attn_res_f8_dequantize(const attn_res_f8_t* q, attn_res_bf16_t* x,
+                                         int64_t x_row, uint32_t flags, void* stream);
+
+/*
+ * attn_res_f8_matmul -- out[m, n] = sum_k a[m, k] w[n, k] for a with row scales
+ * and w with row or block scales, out [a->rows, w->rows]; with a2 and w2 (both
+ * or neither; rows and kinds of block as a's and w's, a width of their own) plus
+ * their product: the gradient of what two projections share, say.  Per block of
+ * 128 columns the codes' products are summed on the tensor cores (tcgen05, fp32)
+ * and then multiplied by the product of the two scales; the blocks' sums are
+ * added in fp32, and the result is rounded once.  (Scales whose product fp32
+ * does not hold are applied by mantissa and exponent: a block's sum is out of
+ * range only if its value is.)  Repeated calls give the same bits.
+ *
+ * out_type: ATTN_RES_OUT_BF16, ATTN_RES_OUT_F32, or ATTN_RES_OUT_F32_ADD, which
+ * adds to the fp32 rows that are there.  fp32 rows: 16-byte aligned, out_row a
+ * multiple of 4.  A width of 0 makes zeros.
+ */
+#define ATTN_RES_OUT_BF16 0
+#define ATTN_RES_OUT_F32 1
+#define ATTN_RES_OUT_F32_ADD 2
+attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t* w,
+                                     const attn_res_f8_t* a2, const attn_res_f8_t* w2, void* out,
+                                     int64_t out_row, int out_type, uint32_t flags, void* stream);
+
+/*
+ * attn_res_f8_gated -- the first half of a gated feed-forward block, both
+ * projections in one kernel:
+ *
+ *   g = x gate^T,  u = x up^T,  h = act(g) * u       [x->rows, gate->rows]
+ *
+ * x with row scales, gate and up of one shape with block scales; products as
+ * attn_res_f8_matmul's, h in fp32 from the fp32 sums.  The result is h in codes
+ * with row scales or, with h NULL, h_rows in bf16.  save_g and save_u (both or
+ * neither) receive g and u in codes with row scales: the checkpoint that
+ * attn_res_f8_gated_backward takes.
+ * activation: ATTN_RES_SILU, act(g) = g / (1 + exp(-g)), or ATTN_RES_GELU, the
+ * tanh form g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, as g / (1 +
+ * exp(-z)) too.  (Fast exponential: act(g) to 2^-16 of itself where it is small,
+ * to a few 2^-23 elsewhere; 0 where exp(-z) overflows, below z = -88.7.)
+ */
+#define ATTN_RES_SILU 1
+#define ATTN_RES_GELU 2
+attn_res_status_t attn_res_f8_gated(const attn_res_f8_t* x, const attn_res_f8_t* gate,
+                                    const attn_res_f8_t* up, int activation,
+                                    const attn_res_f8_t* h, attn_res_bf16_t* h_rows, int64_t h_row,
+                                    const attn_res_f8_t* save_g, const attn_res_f8_t* save_u,
+                                    uint32_t flags, void* stream);
+
+/*
+ * attn_res_f8_gated_backward -- from the gradient dh [T, F] of h and the saved g
+ * and u (row scales), in fp32:
+ *
+ *   dg = dh * u * act'(g),  du = dh * act(g),  h = act(g) * u
+ *
+ * dg and du in codes with row scales, for the input's gradient dx = dg gate + du
+ * up (attn_res_f8_matmul of them and the transposed weights); and, if not NULL
+ * (all three or none), the transposed dg_t, du_t and h_t [F, T], quantised by
+ * themselves in groups along the tokens, for the gradients of the weights.
+ */
+attn_res_status_t attn_res_f8_gated_backward(const attn_res_bf16_t* dh, int64_t dh_row,
+                                             const attn_res_f8_t* g, const attn_res_f8_t* u,
+                                             int activation, const attn_res_f8_t* dg,
+                                             const attn_res_f8_t* du, const attn_res_f8_t* dg_t,
+                                             const attn_res_f8_t* du_t, const attn_res_f8_t* h_t,
+                                             uint32_t flags, void* stream);
+
 /* Static text for a status code. */
 const char* attn_res_status_string(attn_res_status_t status);
 
