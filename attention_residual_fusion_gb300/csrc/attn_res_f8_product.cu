@@ -24,21 +24,6 @@ cudaError_t codes_map(const attn_res_f8_t& x, uint32_t rows, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Of its row scales: boxes of `rows` rows' scales of one block of columns.
-cudaError_t row_scales_map(const attn_res_f8_t& x, uint32_t rows, CUtensorMap* map) {
-  EncodeTiled enc;
-  cudaError_t e = encode_tiled(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dim[2] = {(cuuint64_t)x.rows, (cuuint64_t)f8_blocks(x.cols)};
-  const cuuint64_t stride[1] = {(cuuint64_t)x.scales_row * 4};
-  const cuuint32_t box[2] = {rows, 1};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, x.scales, dim, stride, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 F8View view(const attn_res_f8_t* q) {
   F8View v = {};
   if (q != nullptr) v = {static_cast<uint8_t*>(q->data), q->scales, q->row_bytes, q->scales_row, q->rows, q->cols};
@@ -114,7 +99,6 @@ struct Wide {
       // (a term of width 0 has no blocks, and maps of nothing are none)
       if (e == cudaSuccess && a != nullptr && a->cols > 0) e = codes_map(*a, 128, &maps.a[t]);
       if (e == cudaSuccess && w != nullptr && w->cols > 0) e = codes_map(*w, 128, &maps.w[t]);
-      if (ROWS_W && e == cudaSuccess && w != nullptr && w->cols > 0) e = row_scales_map(*w, C::TN, &maps.w_sf[t]);
     };
     operands(0, c.a, c.w);
     operands(1, c.a2, c.w2);

@@ -8,6 +8,8 @@
 // sum and the sums over blocks in fp32.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_res_f8.cuh"
 #include "attn_res_tcgen05.cuh"
 
@@ -40,7 +42,8 @@ __device__ __forceinline__ void f8_block(uint32_t acc, uint32_t p_lo, uint32_t q
     mma_f8<G>(acc, desc_of(p_lo + 2 * j, kOperandHi), desc_of(q_lo + 2 * j, kOperandHi), idesc, j > 0);
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
@@ -53,33 +56,41 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// ---- scales -------------------------------------------------------------------------------
-
-// The product of two scales where fp32 does not hold it (scales of 1e-30 and
-// 1e-20, say, under which a sum may well be a number, or of 1e25 both, and a
-// sum of 0): mantissas and exponents apart, applied to x as three factors, none
-// of which takes it out of range unless the result is (|x| is 0 or between
-// 2^-18 and 2^26).
-struct FarScale {
-  float mantissa, first, second;
-  __device__ __forceinline__ FarScale(float a, float w) {
-    int ea, ew;
-    mantissa = frexpf(a, &ea) * frexpf(w, &ew);
-    const bool number = fabsf(mantissa) < __int_as_float(0x7f800000);
-    const int e = number ? ea + ew : 0;  // (an infinity's or a NaN's exponent says nothing)
-    const int e1 = min(max(e, -100), 100), e2 = min(max(e - e1, -149), 127);
-    first = ldexpf(1.f, e1);
-    second = ldexpf(1.f, e2);
-  }
-  __device__ __forceinline__ float of(float x) const { return x * mantissa * first * second; }
-};
-__device__ __forceinline__ bool scale_held(float f) {
-  return fabsf(f) >= 0x1p-126f && fabsf(f) < __int_as_float(0x7f800000);
-}
-
 // ---- parameters ---------------------------------------------------------------------------
 
 constexpr int kF8OutBf16 = 0, kF8OutF32 = 1, kF8GatedCodes = 2, kF8GatedBf16 = 3;
+
+// Four neighbours' scales from `at` on (a multiple of 4; 16-byte aligned), 1 past
+// the last.
+__device__ __forceinline__ void ld_scales4(const float* s, int64_t at, int64_t n, float* v) {
+  if (at + 4 <= n) {
+    const float4 x = *reinterpret_cast<const float4*>(s + at);
+    v[0] = x.x;
+    v[1] = x.y;
+    v[2] = x.z;
+    v[3] = x.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = at + k < n ? s[at + k] : 1.f;
+  }
+}
+__device__ __forceinline__ void st_shared4(uint32_t at, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ float ld_shared(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ld_shared_pairs(uint32_t at, f32x2 (&v)[2]) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(at) : "memory");
+}
 
 struct F8Scales {
   const float* at;
@@ -100,7 +111,7 @@ struct F8ProductParams {
 };
 
 struct F8ProductMaps {
-  CUtensorMap a[2], w[2], w_sf[2];
+  CUtensorMap a[2], w[2];
 };
 
 // ---- many tokens: CTA pairs ----------------------------------------------------------------
@@ -108,34 +119,60 @@ struct F8ProductMaps {
 // A pair of CTAs (cta_group::2) makes 256 tokens x 256 columns (of the gated
 // block: 128 of the gate and the same 128 of the up-projection); each holds 128
 // tokens' rows and half of the weight rows.  Persistent pairs walk the tiles;
-// warp 0 loads, warp 1 of the first CTA issues the MMAs of both, warp 2 loads
-// column scales, and eight warps scale and add: each block of K gets an
-// accumulator of 256 TMEM columns of its own, two of which take turns, so that
-// one is read while the tensor cores fill the other.  A thread holds 128 sums:
-// 64 columns of the tile's first half and the same 64 of its second.
+// warp 0 loads, warp 1 of the first CTA issues the MMAs of both, warp 2 makes
+// the scales, and eight warps scale and add.
+//
+// Each block of K gets an accumulator of 256 columns of its own, read while the
+// tensor cores fill the other one.  A thread holds 128 sums: of 128 neighbouring
+// columns (part 0 or 1 of the tile's two blocks of columns) or, gated, of 64 of
+// the gate and the same 64 of the up-projection.
+//
+// The eight warps' way through a block bounds this more than the tensor cores
+// (515 clocks a block): a look at a barrier takes about 80 clocks, an arrival
+// 40, the loads of 64 columns 60 and their additions 70, one after the other.
+// So a block has one wait and one arrival, scales come for four blocks at a
+// time, and the loads of its second half are under way while the first half is
+// added.
 struct F8WideCfg {
   static constexpr int TM = 256, TN = 256;
   static constexpr uint32_t A_BYTES = 128 * 128, W_BYTES = 128 * 128, STAGE = A_BYTES + W_BYTES;
   static constexpr int STAGES = 6;
-  static constexpr int SF_RING = 8;  // blocks of column scales
-  static constexpr uint32_t SF_BYTES = TN * 4;
-  static constexpr uint32_t SMEM = STAGES * STAGE + SF_RING * SF_BYTES + 1024;
+  // Scales, a ring of groups of four blocks of K.  w with block scales: for each
+  // of the tile's two blocks of columns and each row the products of their
+  // scales, four together.  w with row scales: the rows' scales, four together,
+  // then block by block those of 256 columns.
+  static constexpr int GROUP = 4, SF_RING = 2;
+  template <bool ROWS_W>
+  struct Sf {
+    static constexpr uint32_t COLUMNS = 128 * 16;  // behind the rows' (ROWS_W)
+    static constexpr uint32_t BYTES = ROWS_W ? COLUMNS + GROUP * TN * 4 : 2 * 128 * 16;
+  };
+  static constexpr uint32_t SMEM = STAGES * STAGE + SF_RING * Sf<true>::BYTES + 1024;
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int COLS = 512, ACC_STEP = 256;
+  static constexpr int ACCS = 2, ACC_COLS = 256, COLS = ACCS * ACC_COLS;
   // registers: 168 a thread at launch, 64512 in all, of which the first
   // warpgroup gives 96 a thread to the other two
   static constexpr int REGS_FEW = 72, REGS_MANY = 216;
   static_assert(128 * REGS_FEW + 256 * REGS_MANY <= 168 * THREADS, "the split of the registers");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(SMEM <= 227 * 1024 && SF_RING == 2, "shared memory; the ring's turns below");
 };
 
-// 64 fp32 columns of a lane's row, `left` of which exist; `whole`: every row
+// N bf16 columns of a lane's row, `left` of which exist; `whole`: every row
 // starts on a 32-byte boundary.
-__device__ __forceinline__ void store_f32_64(float* o, const f32x2* v, int left, bool whole, bool add) {
-  if (whole && left >= 64) {
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t* o, const f32x2* x, int left, bool whole) {
+  uint32_t v[N / 2];
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
+  for (int e = 0; e < N / 2; ++e) v[e] = pack_bf16x2(f2_lo(x[e]), f2_hi(x[e]));
+  store_row<N>(o, v, left, whole);
+}
+// N fp32 columns; `add`: to what is there.
+template <int N>
+__device__ __forceinline__ void store_f32(float* o, const f32x2* v, int left, bool whole, bool add) {
+  if (whole && left >= N) {
+#pragma unroll
+    for (int k = 0; k < N / 2; k += 4) {
       float e[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -157,21 +194,21 @@ __device__ __forceinline__ void store_f32_64(float* o, const f32x2* v, int left,
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 64; ++k)
+    for (int k = 0; k < N; ++k)
       if (k < left) o[k] = (k % 2 ? f2_hi(v[k / 2]) : f2_lo(v[k / 2])) + (add ? o[k] : 0.f);
   }
 }
 
 // 64 values of a lane's row in codes, over the scale of all 128 columns of the
-// row, whose other half another warp holds: `other` exchanges the bits of the
-// amax.  Columns behind the last hold 0 (or, with their whole row, NaN).
+// row, whose other half another warp holds: `other` gives the bits of the amax
+// of both.  Columns behind the last hold 0 (or, with their whole row, NaN).
 template <class Other>
-__device__ __forceinline__ void store_f8_64(const F8View& q, int64_t row, int64_t col, bool stores, const f32x2* v,
-                                            Other other) {
+__device__ __forceinline__ void store_f8(const F8View& q, int64_t row, int64_t col, bool stores, const f32x2* v,
+                                         Other other) {
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < 32; ++k) m = max(m, max(magnitude(f2_lo(v[k])), magnitude(f2_hi(v[k]))));
-  const F8Scale s = f8_scale(max(m, other(m)));
+  const F8Scale s = f8_scale(other(m));
   if (!stores || row >= q.rows) return;
   if (col % kF8Block == 0) q.scales[col / kF8Block * q.scales_row + row] = s.by;
   uint8_t* const o = q.data + row * q.row_bytes + col;
@@ -196,21 +233,22 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
     attn_res_f8_wide_kernel(const __grid_constant__ F8ProductParams p, const TileWalk walk,
                             const __grid_constant__ F8ProductMaps maps) {
   using C = F8WideCfg;
-  constexpr int S = C::STAGES, R = C::SF_RING;
+  constexpr int S = C::STAGES, R = C::SF_RING, A = C::ACCS;
+  using Sf = typename C::template Sf<ROWS_W>;
   constexpr bool GATED = OUT == kF8GatedCodes || OUT == kF8GatedBf16;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) unsigned long long bars[2 * S + 5 + 2 * R];
+  __shared__ __align__(8) unsigned long long bars[2 * S + 2 * A + 1 + 2 * R];
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t xch[2][2][128];  // [turn][half][row]: amaxes that two warps share
+  __shared__ uint32_t xch[2][2][128];  // [turn][part][row]: amaxes of the warps that share a row
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t full = smem_addr(bars), empty = full + 8 * S, acc_full = empty + 8 * S, acc_empty = acc_full + 16,
-                 drained = acc_empty + 16, sf_full = drained + 8, sf_empty = sf_full + 8 * R;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * S, acc_full = empty + 8 * S, acc_empty = acc_full + 8 * A,
+                 drained = acc_empty + 8 * A, sf_full = drained + 8, sf_empty = sf_full + 8 * R;
   const uint32_t a_at = base, w_at = base + S * C::A_BYTES, sf_at = base + S * C::STAGE;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * S + 2; ++i) mbar_init(full + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(acc_empty + 8 * i, 2 * C::EPI_WARPS);
+    for (int i = 0; i < 2 * S + A; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < A; ++i) mbar_init(acc_empty + 8 * i, 2 * C::EPI_WARPS);
     mbar_init(drained, 1);
     for (int i = 0; i < R; ++i) {
       mbar_init(sf_full + 8 * i, 1);
@@ -263,21 +301,21 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
       bool failed = false;
       int s = 0;
       uint32_t use = 0, it = 0;
-      constexpr uint32_t idesc = f8_idesc(C::TM, C::TN);
+      constexpr uint32_t idesc = f8_idesc(C::TM, C::ACC_COLS);
       const bool issuer = elect_one();
       const uint32_t a_lo = desc_lo(a_at), w_lo = desc_lo(w_at);
       for (int i = first; i < tiles && !failed; i += step) {
         for (int k = 0; k < blocks; ++k, ++it) {
-          const uint32_t b = it & 1;
+          const uint32_t acc = it & 1;
           phase_or_flag(full + 8 * s, use & 1, failed, p.err, kErrStageTimeout);
-          if (it >= 2) phase_or_flag<true>(acc_empty + 8 * b, ((it >> 1) - 1) & 1, failed, p.err, kErrExchangeTimeout);
+          if (it >= 2) phase_or_flag<true>(acc_empty + 8 * acc, ((it >> 1) - 1) & 1, failed, p.err, kErrExchangeTimeout);
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
           tmem_fence_after();
           if (issuer) {
-            f8_block<2>(tmem + b * C::ACC_STEP, a_lo + s * (C::A_BYTES >> 4), w_lo + s * (C::W_BYTES >> 4), idesc);
+            f8_block<2>(tmem + acc * C::ACC_COLS, a_lo + s * (C::A_BYTES >> 4), w_lo + s * (C::W_BYTES >> 4), idesc);
+            mma_commit<2>(acc_full + 8 * acc);
             mma_commit<2>(empty + 8 * s);
-            mma_commit<2>(acc_full + 8 * b);
           }
           __syncwarp();
           if (++s == S) {
@@ -292,195 +330,205 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
         (void)phase_wait(drained, 0);
         drain_stages<S>(full, s, use);
       }
-    } else if (ROWS_W && warp == 2 && lane == 0) {
+    } else if (warp == 2) {
       bool failed = false;
-      uint32_t it = 0;
+      uint32_t group = 0;
       for (int i = first; i < tiles && !failed; i += step) {
         int mt, nt;
         tile_at(walk, i, mt, nt);
-        for (int k = 0; k < blocks; ++k, ++it) {
-          const uint32_t r = it % R;
-          if (it >= R) phase_or_flag(sf_empty + 8 * r, (it / R - 1) & 1, failed, p.err, kErrStageTimeout);
+        const int64_t row = (int64_t)mt * C::TM + rank * 128 + 4 * lane, col = (int64_t)nt * C::TN + 4 * lane;
+        for (int k4 = 0; k4 < blocks; k4 += C::GROUP, ++group) {
+          float a[4][4], w[4][ROWS_W ? 8 : 2];  // [block]; 1 behind the last
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = k4 + j;
+            const bool one = k < blocks0;
+            const int64_t kb = one ? k : k - blocks0;
+            const F8Scales& sa = p.a[one ? 0 : 1];
+            const F8Scales& sw = p.w[one ? 0 : 1];
+            ld_scales4(sa.at + kb * sa.row, row, k < blocks ? p.m : 0, a[j]);
+            if constexpr (ROWS_W) {
+              ld_scales4(sw.at + kb * sw.row, col, k < blocks ? p.n : 0, &w[j][0]);
+              ld_scales4(sw.at + kb * sw.row, col + 128, k < blocks ? p.n : 0, &w[j][4]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const F8Scales& sh = GATED ? p.w[h] : sw;
+                const int64_t at = GATED ? nt : 2 * (int64_t)nt + h;
+                w[j][h] = k < blocks && at * 128 < p.n ? sh.at[at * sh.row + kb] : 1.f;
+              }
+            }
+          }
+          const uint32_t r = group % R, slot = sf_at + r * Sf::BYTES;
+          if (group >= R) phase_or_flag(sf_empty + 8 * r, (group / R - 1) & 1, failed, p.err, kErrStageTimeout);
+          failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
-          const int t = k < blocks0 ? 0 : 1, kb = k < blocks0 ? k : k - blocks0;
-          mbar_arrive_expect_tx(sf_full + 8 * r, C::SF_BYTES);
-          tma_load_2d(sf_at + r * C::SF_BYTES, &maps.w_sf[t], nt * C::TN, kb, sf_full + 8 * r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t at = slot + 16 * (4 * lane + e);
+            if constexpr (ROWS_W) {
+              st_shared4(at, a[0][e], a[1][e], a[2][e], a[3][e]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                st_shared4(slot + Sf::COLUMNS + C::TN * 4 * e + 512 * h + 16 * lane, w[e][4 * h], w[e][4 * h + 1],
+                           w[e][4 * h + 2], w[e][4 * h + 3]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                st_shared4(at + 128 * 16 * h, a[0][e] * w[0][h], a[1][e] * w[1][h], a[2][e] * w[2][h], a[3][e] * w[3][h]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sf_full + 8 * r);
         }
       }
-      if (failed)
-        for (uint32_t b = it > R ? it - R : 0; b < it; ++b) (void)phase_wait(sf_full + 8 * (b % R), (b / R) & 1);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MANY));
     bool failed = false;
     const int q = warp % 4, part = (warp - 4) / 4;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 64 * part;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + (GATED ? 64 : 128) * part;
     const uint32_t release = map_rank(acc_empty, 0);
-    uint32_t it = 0, turn = 0;
+    // whole sectors: every row starts on a 32-byte boundary
+    const bool wide = p.out_row % (OUT == kF8OutF32 ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+    uint32_t it = 0, group = 0, turn = 0;
     // (a warp whose wait has given up goes on through the tiles, without waits
     // or stores: another warp meets it at the exchanges)
     for (int i = first; i < tiles; i += step) {
       int mt, nt;
       tile_at(walk, i, mt, nt);
       const int64_t row = (int64_t)mt * C::TM + rank * 128 + 32 * q + lane;
-      // the scales of this lane's row (1 past the last) and of the tile's
-      // halves, for block k of K
-      auto row_scale = [&](int k) {
-        const bool one = k < blocks0;
-        const F8Scales& s = p.a[one ? 0 : 1];
-        return row < p.m && k < blocks ? s.at[(int64_t)(one ? k : k - blocks0) * s.row + row] : 1.f;
-      };
-      auto block_scale = [&](int k, int half) {
-        const bool one = k < blocks0;
-        const F8Scales& s = p.w[GATED ? half : one ? 0 : 1];
-        const int64_t at = GATED ? nt : 2 * (int64_t)nt + half;
-        return at * 128 < p.n && k < blocks ? s.at[at * s.row + (one ? k : k - blocks0)] : 1.f;
-      };
       f32x2 sum[64];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = f2_make(0.f, 0.f);
-      float ahead[4], sw[2], sw_ahead[2] = {1.f, 1.f};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ahead[j] = row_scale(j);
-      if (!ROWS_W)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) sw_ahead[h] = block_scale(lane, h);
-      for (int k4 = 0; k4 < blocks && !failed; k4 += 4) {
-        float sa[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sa[j] = ahead[j];
-          ahead[j] = row_scale(k4 + 4 + j);
+      for (int e = 0; e < 64; ++e) sum[e] = f2_make(0.f, 0.f);
+      // A wait is one look in the common case, and nothing else lies on the way.
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (phase_done(bar, parity) || failed) return;
+        if (!phase_wait(bar, parity)) {
+          failed = true;
+          atomicOr(p.err, kErrStageTimeout);
         }
-        if (!ROWS_W && k4 % 32 == 0)  // lane l holds those of block k4 + l
+      };
+      // this row's factors in a group of scales (gated: gate's, and behind them up's)
+      const uint32_t mine = sf_at + 16 * (32 * q + lane) + (ROWS_W || GATED ? 0 : 128 * 16 * part);
+      uint32_t v[2][32];
+      float f[2], f_next[2];
+      auto load = [&](uint32_t block, int piece) {
+        tmem_ld(lanes + (block & 1) * C::ACC_COLS + (GATED ? 128 * (piece / 2) + 32 * (piece % 2) : 32 * piece), v[piece % 2]);
+      };
+      auto loaded = [&]() {
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+      };
+      auto factors = [&](uint32_t in_group) {
+        if (in_group == 0) wait(sf_full + 8 * (group & 1), (group >> 1) & 1);
+        const uint32_t at = mine + (group & 1) * Sf::BYTES + 4 * in_group;
+        f_next[0] = ld_shared(at);
+        f_next[1] = GATED ? ld_shared(at + 128 * 16) : f_next[0];
+      };
+      if (blocks > 0) {
+        factors(0);
+        wait(acc_full + 8 * (it & 1), (it >> 1) & 1);
+        __syncwarp();
+        tmem_fence_after();
+        load(it, 0);
+        load(it, 1);
+      }
+#pragma unroll 1
+      for (int k = 0; k < blocks; ++k) {
+        const uint32_t in_group = k % C::GROUP;
+        const bool last = k == blocks - 1, leaves = in_group == C::GROUP - 1 || last;
+        const uint32_t columns = sf_at + (group & 1) * Sf::BYTES + Sf::COLUMNS + C::TN * 4 * in_group + 512 * part;
+        f[0] = f_next[0];
+        f[1] = f_next[1];
+        auto add = [&](int piece) {
+          const f32x2 by = f2_make(f[piece / 2], f[piece / 2]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            sw[h] = sw_ahead[h];
-            sw_ahead[h] = block_scale(k4 + 32 + lane, h);
+          for (int e = 0; e < 16; e += 2) {
+            f32x2 s[2] = {};
+            if constexpr (ROWS_W) ld_shared_pairs(columns + 128 * piece + 8 * e, s);
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const uint32_t* const x = &v[piece % 2][2 * (e + o)];
+              const f32x2 y = f2_make(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              sum[16 * piece + e + o] = f2_fma(y, ROWS_W ? f2_mul(s[o], by) : by, sum[16 * piece + e + o]);
+            }
           }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = k4 + j;
-          if (k >= blocks) break;
-          const uint32_t b = it & 1, r = it % R;
-          if (ROWS_W) phase_or_flag(sf_full + 8 * r, (it / R) & 1, failed, p.err, kErrStageTimeout);
-          phase_or_flag(acc_full + 8 * b, (it >> 1) & 1, failed, p.err, kErrStageTimeout);
-          failed = __any_sync(0xffffffffu, failed);
+        };
+        loaded();
+        add(0);
+        load(it, 2);
+        add(1);
+        load(it, 3);
+        loaded();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_remote(release + 8 * (it & 1));
+          if (!ROWS_W && leaves) mbar_arrive(sf_empty + 8 * (group & 1));
+        }
+        ++it;
+        if (!ROWS_W) group += leaves;
+        // the next block's look at its barrier and its first loads lie among
+        // the additions
+        const uint32_t next = acc_full + 8 * (it & 1);
+        bool there = true;
+        if (!last) {
+          if (!ROWS_W) factors((k + 1) % C::GROUP);
+          there = phase_done(next, (it >> 1) & 1);
+        }
+        add(2);
+        if (!last) {
+          if (!there) wait(next, (it >> 1) & 1);
+          __syncwarp();
           tmem_fence_after();
-          float f[2] = {1.f, 1.f};
-          float w_of[2] = {1.f, 1.f};
-          bool far = false;
-          if constexpr (!ROWS_W) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              w_of[h] = __shfl_sync(0xffffffffu, sw[h], k & 31);
-              f[h] = sa[j] * w_of[h];
-              far |= !scale_held(f[h]);
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              float s;
-              const uint32_t at = sf_at + r * C::SF_BYTES + (64 * part + (h / 2) * 128 + (h % 2) * 32 + lane) * 4;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(at) : "memory");
-              // (0: past the last column)
-              far |= !(fabsf(s) >= 0x1p-100f && fabsf(s) <= 0x1p100f) && s != 0.f;
-            }
-          }
-          far = __any_sync(0xffffffffu, far);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int h = c / 2;
-            uint32_t v[32];
-            tmem_ld32(lanes + b * C::ACC_STEP + 128 * h + 32 * (c % 2), v);
-            tmem_ld_wait(v);
-            if (c == 3) {
-              tmem_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote(release + 8 * b);
-            }
-            const uint32_t sf = sf_at + r * C::SF_BYTES + (64 * part + 128 * h + 32 * (c % 2)) * 4;
-            if (!far) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const f32x2 x = f2_make(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-                if constexpr (!ROWS_W) {
-                  sum[16 * c + e] = f2_fma(x, f2_make(f[h], f[h]), sum[16 * c + e]);
-                } else {
-                  f32x2 s;
-                  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s) : "r"(sf + 8 * e) : "memory");
-                  sum[16 * c + e] = f2_fma(f2_mul(x, s), f2_make(sa[j], sa[j]), sum[16 * c + e]);
-                }
-              }
-            } else {
-              FarScale fs(sa[j], w_of[h]);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float y[2];
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                  if constexpr (ROWS_W) {
-                    float s;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(sf + 8 * e + 4 * o) : "memory");
-                    fs = FarScale(sa[j], s);
-                  }
-                  y[o] = fs.of(__uint_as_float(v[2 * e + o]));
-                }
-                sum[16 * c + e] = f2_make(f2_lo(sum[16 * c + e]) + y[0], f2_hi(sum[16 * c + e]) + y[1]);
-              }
-            }
-          }
-          if (ROWS_W) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sf_empty + 8 * r);
-          }
-          ++it;
+          load(it, 0);
+        }
+        add(3);
+        if (!last) load(it, 1);
+        if constexpr (ROWS_W) {
+          __syncwarp();
+          if (lane == 0 && leaves) mbar_arrive(sf_empty + 8 * (group & 1));
+          group += leaves;
+          if (!last) factors((k + 1) % C::GROUP);
         }
       }
+      failed = __any_sync(0xffffffffu, failed);
       if (i + step >= tiles) grid_dep_launch_dependents();
-      if constexpr (OUT == kF8OutBf16 || OUT == kF8OutF32) {
+      if constexpr (!GATED) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int64_t col = (int64_t)nt * C::TN + 128 * h + 64 * part;
+          const int64_t col = (int64_t)nt * C::TN + 128 * part + 64 * h;
           if (failed || row >= p.m || col >= p.n) continue;
           const int left = (int)(p.n - col < 64 ? p.n - col : 64);
-          if constexpr (OUT == kF8OutBf16) {
-            const bool wide = p.out_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-            uint32_t v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = pack_bf16x2(f2_lo(sum[32 * h + e]), f2_hi(sum[32 * h + e]));
-            store_row64(static_cast<uint16_t*>(p.out) + row * p.out_row + col, v, left, wide);
-          } else {
-            const bool whole = p.out_row % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-            store_f32_64(static_cast<float*>(p.out) + row * p.out_row + col, sum + 32 * h, left, whole, p.add);
-          }
+          if constexpr (OUT == kF8OutBf16)
+            store_bf16<64>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide);
+          else
+            store_f32<64>(static_cast<float*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide, p.add);
         }
       } else {
         const int64_t col = (int64_t)nt * 128 + 64 * part;
-        // the other half's amax of the same row
+        // the amax of this row's values and the other part's
         auto other = [&](uint32_t m) {
           uint32_t(&x)[2][128] = xch[turn++ & 1];
           x[part][32 * q + lane] = m;
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-          return x[1 - part][32 * q + lane];
+          return max(m, x[1 - part][32 * q + lane]);
         };
         const bool stores = !failed && col < p.n;
-        if (p.g.data) store_f8_64(p.g, row, col, stores, sum, other);
-        if (p.u.data) store_f8_64(p.u, row, col, stores, sum + 32, other);
+        if (p.g.data) store_f8(p.g, row, col, stores, sum, other);
+        if (p.u.data) store_f8(p.u, row, col, stores, sum + 32, other);
+        f32x2* const h = sum;
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float lo = f8_act<ACT>(f2_lo(sum[e])), hi = f8_act<ACT>(f2_hi(sum[e]));
-          sum[e] = f2_mul(f2_make(lo, hi), sum[32 + e]);
+          const float lo = f8_act<ACT>(f2_lo(h[e])), hi = f8_act<ACT>(f2_hi(h[e]));
+          h[e] = f2_mul(f2_make(lo, hi), h[32 + e]);
         }
         if constexpr (OUT == kF8GatedCodes) {
-          store_f8_64(p.h, row, col, stores, sum, other);
+          store_f8(p.h, row, col, stores, h, other);
         } else if (stores && row < p.m) {
-          const bool wide = p.out_row % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-          uint32_t v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = pack_bf16x2(f2_lo(sum[e]), f2_hi(sum[e]));
-          store_row64(static_cast<uint16_t*>(p.out) + row * p.out_row + col, v,
-                      (int)(p.n - col < 64 ? p.n - col : 64), wide);
+          store_bf16<64>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, h,
+                         (int)(p.n - col < 64 ? p.n - col : 64), wide);
         }
       }
     }
