@@ -112,18 +112,28 @@ template <int ACT>
 __device__ __forceinline__ float f8_act(float g) {
   return g * f8_sigmoid(f8_gate_arg<ACT>(g));
 }
-// act(g) and its derivative p + g p (1 - p) z'(g).  The derivative is taken of
-// g held to +-100, where it is 1 or 0, so that z' stays a number (at 1e19 0 x
-// inf would come of it).
+// act(g) and its derivative p + g p (1 - p) z'(g) of a pair.  The derivative is
+// taken of g held to +-100, where it is 1 or 0, so that z' stays a number (at
+// 1e19 0 x inf would come of it).
 template <int ACT>
-__device__ __forceinline__ void f8_act_both(float g, float& act, float& slope) {
-  const float c = fminf(fmaxf(g, -100.f), 100.f);
-  const float p = f8_sigmoid(f8_gate_arg<ACT>(c));
-  act = g * p;
-  float dz = 1.f;
-  if constexpr (ACT != ATTN_RES_SILU) dz = kGeluScale * fmaf(3.f * kGeluCubic * c, c, 1.f);
-  slope = fmaf(c * p * (1.f - p), dz, p);
-  if (g != g) slope = g;  // (fminf and fmaxf drop a NaN)
+__device__ __forceinline__ void f8_act_both2(f32x2 g, f32x2& act, f32x2& slope) {
+  float c[2], p[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float x = e ? f2_hi(g) : f2_lo(g);
+    // (not fminf and fmaxf, which drop a NaN)
+    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, 0f42C80000;\n\tmax.NaN.f32 %0, t, 0fC2C80000;\n\t}" : "=f"(c[e]) : "f"(x));
+    p[e] = f8_sigmoid(f8_gate_arg<ACT>(c[e]));
+  }
+  const f32x2 c2 = f2_make(c[0], c[1]), p2 = f2_make(p[0], p[1]);
+  act = f2_mul(g, p2);
+  const f32x2 minus = f2_make(-1.f, -1.f), one = f2_make(1.f, 1.f);
+  f32x2 t = f2_mul(f2_mul(c2, p2), f2_fma(p2, minus, one));
+  if constexpr (ACT != ATTN_RES_SILU) {
+    const float q = 3.f * kGeluCubic * kGeluScale;
+    t = f2_mul(t, f2_fma(f2_mul(c2, f2_make(q, q)), c2, f2_make(kGeluScale, kGeluScale)));
+  }
+  slope = f2_fma(t, one, p2);
 }
 
 }  // namespace attn_res_dev

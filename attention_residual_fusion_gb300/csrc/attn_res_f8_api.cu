@@ -4,6 +4,7 @@
 // every check passes.
 #include "attn_res_f8_host.cuh"
 #include "attn_res_f8_rows.cuh"
+#include "attn_res_tensor_host.cuh"
 
 namespace {
 
@@ -79,6 +80,23 @@ attn_res_status_t run(void (*kern)(Params...), int64_t ctas, void* stream, const
   if (st != ATTN_RES_OK) return st;
   Launch l(ctas, kF8Threads, stream);
   return launched(cudaLaunchKernelEx(&l.cfg, kern, p...));
+}
+
+template <int ACT, bool TRANSPOSED>
+cudaError_t launch_backward(const F8BackwardParams& p, const F8BackwardMaps& maps, int device, void* stream) {
+  const auto kern = attn_res_f8_gated_backward_kernel<ACT, TRANSPOSED>;
+  static std::atomic<uint64_t> enabled{0};
+  static std::atomic<int> sms[64];
+  cudaError_t e = allow_smem(kern, sizeof(F8BackShared), device, enabled);
+  int ctas = sms[device].load(std::memory_order_acquire);
+  if (e == cudaSuccess && ctas == 0) {
+    e = cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) sms[device].store(ctas, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  Launch l(p.tiles < ctas ? p.tiles : ctas, kF8BackThreads, stream);
+  l.cfg.dynamicSmemBytes = sizeof(F8BackShared);
+  return cudaLaunchKernelEx(&l.cfg, kern, p, maps);
 }
 
 }  // namespace
@@ -238,13 +256,24 @@ attn_res_status_t attn_res_f8_gated_backward(const attn_res_bf16_t* dh, int64_t 
   for (const attn_res_f8_t* q : {g, u}) spans.add(q, false);
   for (const attn_res_f8_t* q : {dg, du, dg_t, du_t, h_t}) spans.add(q, true);
   if (spans.clash()) return ATTN_RES_EALIAS;
-  const int64_t ctas = tile_ctas(T, F);
-  if (ctas < 0) return ATTN_RES_EINVAL;
+  const int64_t tiles = tile_ctas(T, F);
+  if (tiles < 0 || tiles > INT32_MAX / 2) return ATTN_RES_EINVAL;
   F8BackwardParams p = {};
-  p.dh = dh;
-  p.dh_row = dh_row;
-  p.gate = view(*g);
-  p.up = view(*u);
+  F8BackwardMaps maps;
+  int device;
+  st = current_device(&device);
+  if (st != ATTN_RES_OK) return st;
+  cudaError_t e = device_status_word(device, &p.err);
+  auto map = [&](CUtensorMapDataType type, const void* at, int64_t cols, int64_t rows, int64_t row_bytes,
+                 uint32_t box_rows, CUtensorMap* m) {
+    if (e == cudaSuccess) e = map_2d(type, at, cols, rows, row_bytes, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE, m);
+  };
+  map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dh, F, T, dh_row * 2, 128, &maps.dh);
+  map(CU_TENSOR_MAP_DATA_TYPE_UINT8, g->data, F, T, g->row_bytes, 128, &maps.g);
+  map(CU_TENSOR_MAP_DATA_TYPE_UINT8, u->data, F, T, u->row_bytes, 128, &maps.u);
+  map(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g->scales, T, f8_blocks(F), g->scales_row * 4, 1, &maps.g_scales);
+  map(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, u->scales, T, f8_blocks(F), u->scales_row * 4, 1, &maps.u_scales);
+  if (e != cudaSuccess) return launched(e);
   p.dg = view(*dg);
   p.du = view(*du);
   if (transposed) {
@@ -252,11 +281,16 @@ attn_res_status_t attn_res_f8_gated_backward(const attn_res_bf16_t* dh, int64_t 
     p.du_t = view(*du_t);
     p.h_t = view(*h_t);
   }
-  if (activation == ATTN_RES_SILU)
-    return transposed ? run(attn_res_f8_gated_backward_kernel<ATTN_RES_SILU, true>, ctas, stream, p)
-                      : run(attn_res_f8_gated_backward_kernel<ATTN_RES_SILU, false>, ctas, stream, p);
-  return transposed ? run(attn_res_f8_gated_backward_kernel<ATTN_RES_GELU, true>, ctas, stream, p)
-                    : run(attn_res_f8_gated_backward_kernel<ATTN_RES_GELU, false>, ctas, stream, p);
+  p.tiles = (int)tiles;
+  p.col_tiles = (int)f8_blocks(F);
+  const bool silu = activation == ATTN_RES_SILU;
+  if (transposed)
+    e = silu ? launch_backward<ATTN_RES_SILU, true>(p, maps, device, stream)
+             : launch_backward<ATTN_RES_GELU, true>(p, maps, device, stream);
+  else
+    e = silu ? launch_backward<ATTN_RES_SILU, false>(p, maps, device, stream)
+             : launch_backward<ATTN_RES_GELU, false>(p, maps, device, stream);
+  return launched(e);
 }
 
 }  // extern "C"

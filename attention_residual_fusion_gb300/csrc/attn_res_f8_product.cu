@@ -8,20 +8,10 @@ namespace {
 
 using namespace attn_res_dev;
 
-// Tensor map of an operand's codes: boxes of 128 bytes x `rows`, 128-byte
-// swizzle; bytes past the row's end and rows past the last read as 0.
+// Tensor map of an operand's codes: boxes of 128 bytes x `rows`, swizzled.
 cudaError_t codes_map(const attn_res_f8_t& x, uint32_t rows, CUtensorMap* map) {
-  EncodeTiled enc;
-  cudaError_t e = encode_tiled(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dim[2] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows};
-  const cuuint64_t stride[1] = {(cuuint64_t)x.row_bytes};
-  const cuuint32_t box[2] = {128, rows};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.data, dim, stride, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return map_2d(CU_TENSOR_MAP_DATA_TYPE_UINT8, x.data, x.cols, x.rows, x.row_bytes, 128, rows,
+                CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 F8View view(const attn_res_f8_t* q) {

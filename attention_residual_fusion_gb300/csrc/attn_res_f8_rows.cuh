@@ -3,6 +3,7 @@
 #pragma once
 
 #include "attn_res_f8.cuh"
+#include "attn_res_tcgen05.cuh"
 
 namespace attn_res_dev {
 
@@ -299,124 +300,219 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_dequantize_kernel(cons
 //
 // From h's gradient and the codes of both projections: dg = dh u act'(g), du =
 // dh act(g), by rows and, for the gradients of the weights, transposed, with
-// the transposed h = act(g) u.  Each value is needed for two scales and two
-// codes: it is made twice, once for the maxima and once for the codes, from
-// the inputs in registers.
+// the transposed h = act(g) u.
+//
+// Nine bytes an element at the copy rate leave an SM some 45 instructions for
+// one, and about as many are needed: a value is made once and stays in
+// registers until both its scales are known (512 threads, 8 rows x 4 columns of
+// a 128 x 128 tile each, 96 values), and codes are made with the scale's
+// inverse.  That leaves room for one CTA an SM, so the CTAs are persistent and
+// the next tile's inputs are brought in by TMA meanwhile.
+constexpr int kF8BackThreads = 512;
+constexpr int kF8BackRows = 8;  // of a warp
+
 struct F8BackwardParams {
-  const uint16_t* dh;
-  int64_t dh_row;
-  F8View gate, up;
-  F8View dg, du;          // by rows
-  F8View dg_t, du_t, h_t;  // transposed; data null: none of the three
+  F8View dg, du;           // by rows
+  F8View dg_t, du_t, h_t;  // transposed
+  int tiles, col_tiles;
+  unsigned* err;
+};
+struct F8BackwardMaps {
+  CUtensorMap dh, g, u, g_scales, u_scales;
+};
+// Shared memory: two stages of inputs, the transposed codes, amaxes and
+// inverses of the columns' scales.
+struct F8BackStage {
+  uint16_t dh[128][128];
+  uint8_t g[128][128], u[128][128];
+  float g_scales[128], u_scales[128];
+};
+struct F8BackShared {
+  F8BackStage stage[2];
+  uint2 codes[3][128][16];  // [dg, du, h][column][8 rows], places mixed
+  uint32_t amax[3][128];
+  float inverse[3][128];
+  unsigned long long full[2];
 };
 
+// The codes of four values with a scale's inverse (NaN: none).
+__device__ __forceinline__ uint32_t codes_by(f32x2 a, f32x2 b) {
+  return e4m3x4(f2_lo(a), f2_hi(a), f2_lo(b), f2_hi(b));
+}
+
 template <int ACT, bool TRANSPOSED>
-__global__ void __launch_bounds__(kF8Threads) attn_res_f8_gated_backward_kernel(const F8BackwardParams p) {
-  __shared__ TileShared sh;
+__global__ void __launch_bounds__(kF8BackThreads, 1)
+    attn_res_f8_gated_backward_kernel(const __grid_constant__ F8BackwardParams p,
+                                      const __grid_constant__ F8BackwardMaps maps) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  F8BackShared& sh = *reinterpret_cast<F8BackShared*>(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t blocks = f8_blocks(p.gate.cols), cols = p.gate.cols;
-  const int64_t rb = blockIdx.x / blocks, cb = blockIdx.x % blocks;
-  const int64_t row0 = rb * kF8Block + warp * kF8Strip, col0 = cb * kF8Block, col = col0 + 4 * lane;
-  const int rows = (int)(p.gate.rows - row0 < kF8Strip ? p.gate.rows - row0 : kF8Strip);
+  const uint32_t full = smem_addr(sh.full);
+  const int64_t rows = p.dg.rows, cols = p.dg.cols;
+  auto load = [&](int tile, int s) {
+    const int row0 = tile / p.col_tiles * 128, col0 = tile % p.col_tiles * 128;
+    const uint32_t bar = full + 8 * s;
+    F8BackStage& to = sh.stage[s];
+    mbar_arrive_expect_tx(bar, sizeof(F8BackStage));
+    tma_load_2d(smem_addr(to.dh), &maps.dh, col0, row0, bar);
+    tma_load_2d(smem_addr(to.g), &maps.g, col0, row0, bar);
+    tma_load_2d(smem_addr(to.u), &maps.u, col0, row0, bar);
+    tma_load_2d(smem_addr(to.g_scales), &maps.g_scales, row0, col0 / 128, bar);
+    tma_load_2d(smem_addr(to.u_scales), &maps.u_scales, row0, col0 / 128, bar);
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(full, 1);
+    mbar_init(full + 8, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 3 * 128) sh.amax[threadIdx.x / 128][threadIdx.x % 128] = 0;
   grid_dep_wait();
-  uint2 dh[kF8Strip];
-  uint32_t g[kF8Strip], u[kF8Strip];
+  __syncthreads();
+  const int first = blockIdx.x, step = gridDim.x;
+  uint32_t issued = 0;  // thread 0's loads
+  if (threadIdx.x == 0)
+    for (int s = 0; s < 2 && first + s * step < p.tiles; ++s, ++issued) load(first + s * step, s);
+  bool failed = false;
+  uint32_t it = 0;
+  for (int tile = first; tile < p.tiles; tile += step, ++it) {
+    const int s = it & 1;
+    const int64_t rb = tile / p.col_tiles, cb = tile % p.col_tiles;
+    const int64_t row0 = rb * 128 + warp * kF8BackRows, col0 = cb * 128, col = col0 + 4 * lane;
+    phase_or_flag(full + 8 * s, (it >> 1) & 1, failed, p.err, kErrStageTimeout);
+    const F8BackStage& in = sh.stage[s];
+    f32x2 dg[kF8BackRows][2], du[kF8BackRows][2], h[kF8BackRows][2];
+    uint32_t am_g = 0, am_u = 0;  // lane i: of row row0 + i
 #pragma unroll
-  for (int i = 0; i < kF8Strip; ++i) {
-    const bool in = i < rows;
-    dh[i] = in ? ld_bf16x4(p.dh + (row0 + i) * p.dh_row, col, cols) : make_uint2(0, 0);
-    g[i] = in ? ld_codes4(p.gate.data + (row0 + i) * p.gate.row_bytes, col, cols) : 0u;
-    u[i] = in ? ld_codes4(p.up.data + (row0 + i) * p.up.row_bytes, col, cols) : 0u;
-  }
-  float sg = 1.f, su = 1.f;  // of row row0 + lane
-  if (lane < rows && lane < kF8Strip) {
-    sg = p.gate.scales[cb * p.gate.scales_row + row0 + lane];
-    su = p.up.scales[cb * p.up.scales_row + row0 + lane];
-  }
-  struct Four {
-    float dg[4], du[4], h[4];
-  };
-  auto values = [&](int i) {
-    const float by_g = __shfl_sync(0xffffffffu, sg, i), by_u = __shfl_sync(0xffffffffu, su, i);
-    Four v;
+    for (int i = 0; i < kF8BackRows; ++i) {
+      const int r = warp * kF8BackRows + i;
+      // (volatile: a row's inputs only when it is their turn, or registers run out)
+      uint2 d;
+      uint32_t gc, uc;
+      float sg, su;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(d.x), "=r"(d.y) : "r"(smem_addr(&in.dh[r][4 * lane])) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(gc) : "r"(smem_addr(&in.g[r][4 * lane])) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uc) : "r"(smem_addr(&in.u[r][4 * lane])) : "memory");
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sg) : "r"(smem_addr(&in.g_scales[r])) : "memory");
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(su) : "r"(smem_addr(&in.u_scales[r])) : "memory");
+      uint32_t a = 0, b = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const f32x2 gv = f2_mul(e4m3_pair(g[i] >> (16 * j)), f2_make(by_g, by_g));
-      const f32x2 uv = f2_mul(e4m3_pair(u[i] >> (16 * j)), f2_make(by_u, by_u));
-      const uint32_t d = j ? dh[i].y : dh[i].x;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float act, slope;
-        f8_act_both<ACT>(k ? f2_hi(gv) : f2_lo(gv), act, slope);
-        const float ue = k ? f2_hi(uv) : f2_lo(uv), de = k ? bf_hi(d) : bf_lo(d);
-        const int e = 2 * j + k;
-        // columns behind the last count for nothing, whatever a row's scale is
-        const bool in = col + e < cols;
-        v.dg[e] = in ? de * ue * slope : 0.f;
-        v.du[e] = in ? de * act : 0.f;
-        v.h[e] = in ? act * ue : 0.f;
+      for (int j = 0; j < 2; ++j) {
+        const f32x2 g = f2_mul(e4m3_pair(gc >> (16 * j)), f2_make(sg, sg));
+        const f32x2 u = f2_mul(e4m3_pair(uc >> (16 * j)), f2_make(su, su));
+        const f32x2 dh = bf2_widen(j ? d.y : d.x);
+        f32x2 act, slope;
+        f8_act_both2<ACT>(g, act, slope);
+        du[i][j] = f2_mul(dh, act);
+        dg[i][j] = f2_mul(f2_mul(dh, u), slope);
+        h[i][j] = f2_mul(act, u);
+        // (rows and columns behind the last were read as zeros: they count for
+        // nothing where the row's scales are numbers, and where one is none the
+        // row's values are none either)
+        a = max(a, max(magnitude(f2_lo(dg[i][j])), magnitude(f2_hi(dg[i][j]))));
+        b = max(b, max(magnitude(f2_lo(du[i][j])), magnitude(f2_hi(du[i][j]))));
+      }
+      a = __reduce_max_sync(0xffffffffu, a);
+      b = __reduce_max_sync(0xffffffffu, b);
+      if (lane == i) {
+        am_g = a;
+        am_u = b;
       }
     }
-    return v;
-  };
-  uint32_t rg[kF8Strip], ru[kF8Strip], cg[4] = {}, cu[4] = {}, ch[4] = {};
+    if constexpr (TRANSPOSED) {
 #pragma unroll
-  for (int i = 0; i < kF8Strip; ++i) {
-    const Four v = values(i);
-    rg[i] = ru[i] = 0;
+      for (int which = 0; which < 3; ++which)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = magnitude(v.dg[j]), b = magnitude(v.du[j]);
-      rg[i] = max(rg[i], a);
-      ru[i] = max(ru[i], b);
-      cg[j] = max(cg[j], a);
-      cu[j] = max(cu[j], b);
-      ch[j] = max(ch[j], magnitude(v.h[j]));
-    }
-  }
-  const StripScales srg(rg), sru(ru);
-  srg.store(p.dg, row0, cb);
-  sru.store(p.du, row0, cb);
+        for (int j = 0; j < 2; ++j) {
+          uint32_t lo = 0, hi = 0;
 #pragma unroll
-  for (int i = 0; i < kF8Strip; ++i) {
-    const Four v = values(i);
-    const F8Scale a = srg.of(i), b = sru.of(i);
-    if (i < rows) {
-      st_codes4(p.dg.data + (row0 + i) * p.dg.row_bytes, col, cols,
-                f8_codes(f2_make(v.dg[0], v.dg[1]), f2_make(v.dg[2], v.dg[3]), a));
-      st_codes4(p.du.data + (row0 + i) * p.du.row_bytes, col, cols,
-                f8_codes(f2_make(v.du[0], v.du[1]), f2_make(v.du[2], v.du[3]), b));
-    }
-  }
-  if constexpr (TRANSPOSED) {
-#pragma unroll
-    for (int which = 0; which < 3; ++which) {
-      const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
-      // (its first barrier: the piece before has been read)
-      tile_column_scales(sh, which == 0 ? cg : which == 1 ? cu : ch, t, col0, rb);
-      F8Scale s[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = sh.scale[4 * lane + j];
-      uint32_t codes[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float v[4][4];  // [row][column]
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const Four f = values(4 * k + i);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = which == 0 ? f.dg[j] : which == 1 ? f.du[j] : f.h[j];
+          for (int i = 0; i < kF8BackRows; ++i) {
+            const f32x2 v = which == 0 ? dg[i][j] : which == 1 ? du[i][j] : h[i][j];
+            lo = max(lo, magnitude(f2_lo(v)));
+            hi = max(hi, magnitude(f2_hi(v)));
+          }
+          atomicMax(&sh.amax[which][4 * lane + 2 * j], lo);
+          atomicMax(&sh.amax[which][4 * lane + 2 * j + 1], hi);
         }
+    }
+    __syncthreads();  // the stage has been read, the columns' maxima are there
+    if (threadIdx.x == 0 && tile + 2 * step < p.tiles && !failed) {
+      load(tile + 2 * step, s);
+      ++issued;
+    }
+    const F8Scale sg = f8_scale(am_g), su = f8_scale(am_u);
+    if (TRANSPOSED && threadIdx.x < 3 * 128) {
+      const int which = threadIdx.x / 128, c = threadIdx.x % 128;
+      const F8Scale sc = f8_scale(sh.amax[which][c]);
+      sh.inverse[which][c] = sc.inverse;
+      sh.amax[which][c] = 0;
+      const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
+      if (col0 + c < cols && !failed) t.scales[rb * t.scales_row + col0 + c] = sc.by;
+    }
+    if (lane < kF8BackRows && row0 + lane < rows && !failed) {
+      p.dg.scales[cb * p.dg.scales_row + row0 + lane] = sg.by;
+      p.du.scales[cb * p.du.scales_row + row0 + lane] = su.by;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) codes[j][k] = f8_codes(f2_make(v[0][j], v[1][j]), f2_make(v[2][j], v[3][j]), s[j]);
+    for (int i = 0; i < kF8BackRows; ++i) {
+      const float ig = __shfl_sync(0xffffffffu, sg.inverse, i), iu = __shfl_sync(0xffffffffu, su.inverse, i);
+      const f32x2 by_g = f2_make(ig, ig), by_u = f2_make(iu, iu);
+      uint32_t a = codes_by(f2_mul(dg[i][0], by_g), f2_mul(dg[i][1], by_g));
+      uint32_t b = codes_by(f2_mul(du[i][0], by_u), f2_mul(du[i][1], by_u));
+      if (ig != ig) a = 0;
+      if (iu != iu) b = 0;
+      if (row0 + i < rows && !failed) {
+        st_codes4(p.dg.data + (row0 + i) * p.dg.row_bytes, col, cols, a);
+        st_codes4(p.du.data + (row0 + i) * p.du.row_bytes, col, cols, b);
       }
+    }
+    if constexpr (TRANSPOSED) {
+      __syncthreads();  // the inverses are there; the codes of the tile before have left
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
+      for (int which = 0; which < 3; ++which) {
+        const float4 inv = *reinterpret_cast<const float4*>(&sh.inverse[which][4 * lane]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float i0 = j ? inv.z : inv.x, i1 = j ? inv.w : inv.y;
+          const f32x2 by = f2_make(i0, i1);
+          f32x2 v[kF8BackRows];
+#pragma unroll
+          for (int i = 0; i < kF8BackRows; ++i) v[i] = f2_mul(which == 0 ? dg[i][j] : which == 1 ? du[i][j] : h[i][j], by);
+          uint2 lo, hi;
+          lo.x = e4m3x4(f2_lo(v[0]), f2_lo(v[1]), f2_lo(v[2]), f2_lo(v[3]));
+          lo.y = e4m3x4(f2_lo(v[4]), f2_lo(v[5]), f2_lo(v[6]), f2_lo(v[7]));
+          hi.x = e4m3x4(f2_hi(v[0]), f2_hi(v[1]), f2_hi(v[2]), f2_hi(v[3]));
+          hi.y = e4m3x4(f2_hi(v[4]), f2_hi(v[5]), f2_hi(v[6]), f2_hi(v[7]));
+          if (i0 != i0) lo = make_uint2(0, 0);
+          if (i1 != i1) hi = make_uint2(0, 0);
+          // column c's piece of warp w at w ^ (c / 4 % 16): writes and reads
+          // without bank conflicts
+          sh.codes[which][4 * lane + 2 * j][warp ^ (lane & 15)] = lo;
+          sh.codes[which][4 * lane + 2 * j + 1][warp ^ (lane & 15)] = hi;
+        }
+      }
       __syncthreads();
-      tile_store_transposed(sh, t, col0, rb * kF8Block);
+      const int64_t at0 = rb * 128;
+      for (int i = threadIdx.x; i < 3 * 128 * 8; i += kF8BackThreads) {
+        const int which = i / (128 * 8), c = i / 8 % 128, piece = i % 8;
+        const int64_t at = at0 + 16 * piece;
+        if (col0 + c >= cols || at >= rows || failed) continue;
+        const int x = (c >> 2) & 15;
+        const uint4 two = *reinterpret_cast<const uint4*>(&sh.codes[which][c][(2 * piece ^ x) & ~1]);
+        const uint4 v = x & 1 ? make_uint4(two.z, two.w, two.x, two.y) : two;
+        const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
+        uint8_t* const o = t.data + (col0 + c) * t.row_bytes + at;
+        if (at + 16 <= rows) {
+          *reinterpret_cast<uint4*>(o) = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (at + k < rows) o[k] = (uint8_t)(vword(v, k / 4) >> (8 * (k % 4)));
+        }
+      }
     }
   }
+  if (failed)  // copies still in flight land before the CTA ends
+    for (uint32_t b = issued > 2 ? issued - 2 : 0; b < issued; ++b) (void)phase_wait(full + 8 * (b & 1), (b >> 1) & 1);
   grid_dep_launch_dependents();
 }
 

@@ -10,33 +10,15 @@ using namespace attn_res_dev;
 // Tensor map of an operand's codes as bytes: boxes of 128 bytes x `rows`,
 // 128-byte swizzle; bytes past the row's end and rows past the last read as 0.
 cudaError_t operand_map(const attn_res_mx_t& x, uint32_t rows, CUtensorMap* map) {
-  EncodeTiled enc;
-  cudaError_t e = encode_tiled(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dim[2] = {(cuuint64_t)(x.cols * mx_bits(x.format) / 8), (cuuint64_t)x.rows};
-  const cuuint64_t stride[1] = {(cuuint64_t)x.row_bytes};
-  const cuuint32_t box[2] = {128, rows};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.data, dim, stride, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return map_2d(CU_TENSOR_MAP_DATA_TYPE_UINT8, x.data, x.cols * mx_bits(x.format) / 8, x.rows, x.row_bytes, 128, rows,
+                CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 // Of its scales: rows of 512 bytes (one tile of 128 rows x 4 groups), boxes of
 // the tiles of one 128-byte block of codes.
 cudaError_t scales_map(const attn_res_mx_t& x, uint32_t tiles, CUtensorMap* map) {
-  EncodeTiled enc;
-  cudaError_t e = encode_tiled(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dim[2] = {128, (cuuint64_t)((x.rows + 127) / 128 * mx_group_tiles(x.format, x.cols))};
-  const cuuint64_t stride[1] = {512};
-  const cuuint32_t box[2] = {128, tiles};
-  const cuuint32_t one[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, x.scales, dim, stride, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return map_2d(CU_TENSOR_MAP_DATA_TYPE_UINT32, x.scales, 128, (x.rows + 127) / 128 * mx_group_tiles(x.format, x.cols),
+                512, 128, tiles, CU_TENSOR_MAP_SWIZZLE_NONE, map);
 }
 
 template <int FMT>
