@@ -43,6 +43,12 @@ attn_res_status_t check_f32_rows(const float* x, int64_t rows, int64_t row, int6
   return ATTN_RES_OK;
 }
 
+constexpr uint32_t kOverrides = ATTN_RES_FLAG_KERNEL(0xf) | ATTN_RES_FLAG_SPLIT(0xff);
+void overrides(uint32_t flags, F8Call* c) {
+  c->kernel = static_cast<int>((flags >> 16) & 0xfu);
+  c->split = static_cast<int>((flags >> 8) & 0xffu);
+}
+
 // The ranges of a call's arguments, two for a matrix.
 template <int N>
 struct Spans {
@@ -152,12 +158,19 @@ attn_res_status_t attn_res_f8_dequantize(const attn_res_f8_t* q, attn_res_bf16_t
 attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t* w, const attn_res_f8_t* a2,
                                      const attn_res_f8_t* w2, void* out, int64_t out_row, int out_type,
                                      uint32_t flags, void* stream) {
-  if (!scalars_ok(a, ATTN_RES_F8_ROWS) || !scalars_ok(w) || a->cols != w->cols || !known_flags(flags) ||
+  if (!scalars_ok(a, ATTN_RES_F8_ROWS) || !scalars_ok(w) || a->cols != w->cols || !known_flags(flags & ~kOverrides) ||
       out_type < ATTN_RES_OUT_BF16 || out_type > ATTN_RES_OUT_F32_ADD || (a2 == nullptr) != (w2 == nullptr))
     return ATTN_RES_EINVAL;
   if (a2 != nullptr && (!scalars_ok(a2, ATTN_RES_F8_ROWS) || !scalars_ok(w2, w->block) || a2->rows != a->rows ||
                         w2->rows != w->rows || a2->cols != w2->cols))
     return ATTN_RES_EINVAL;
+  F8Call c = {};
+  c.a = a;
+  c.w = w;
+  c.a2 = a2;
+  c.w2 = w2;
+  overrides(flags, &c);
+  if (!f8_overrides_ok(c)) return ATTN_RES_EINVAL;
   if (a->rows == 0 || w->rows == 0) return ATTN_RES_OK;
   attn_res_status_t st = check_matrix(*a);
   if (st == ATTN_RES_OK) st = check_matrix(*w);
@@ -175,15 +188,10 @@ attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t
   spans.add(a2, false);
   spans.add(w2, false);
   if (spans.clash()) return ATTN_RES_EALIAS;
-  F8Call c = {};
   st = current_device(&c.device);
   if (st != ATTN_RES_OK) return st;
   cudaError_t e = device_status_word(c.device, &c.err);
   if (e != cudaSuccess) return launched(e);
-  c.a = a;
-  c.w = w;
-  c.a2 = a2;
-  c.w2 = w2;
   c.out = out;
   c.out_row = out_row;
   c.out_type = out_type;
@@ -197,12 +205,19 @@ attn_res_status_t attn_res_f8_gated(const attn_res_f8_t* x, const attn_res_f8_t*
                                     const attn_res_f8_t* save_g, const attn_res_f8_t* save_u, uint32_t flags,
                                     void* stream) {
   if (!scalars_ok(x, ATTN_RES_F8_ROWS) || !scalars_ok(gate, ATTN_RES_F8_SQUARE) || gate->cols != x->cols ||
-      !shaped(up, ATTN_RES_F8_SQUARE, gate->rows, gate->cols) || !known_activation(activation) || !known_flags(flags) ||
-      (h != nullptr && h_rows != nullptr) || (save_g == nullptr) != (save_u == nullptr))
+      !shaped(up, ATTN_RES_F8_SQUARE, gate->rows, gate->cols) || !known_activation(activation) ||
+      !known_flags(flags & ~kOverrides) || (h != nullptr && h_rows != nullptr) || (save_g == nullptr) != (save_u == nullptr))
     return ATTN_RES_EINVAL;
   const int64_t T = x->rows, F = gate->rows;
   for (const attn_res_f8_t* q : {h, save_g, save_u})
     if (q != nullptr && !shaped(q, ATTN_RES_F8_ROWS, T, F)) return ATTN_RES_EINVAL;
+  F8Call c = {};
+  c.a = x;
+  c.w = gate;
+  c.w2 = up;
+  c.gated = true;
+  overrides(flags, &c);
+  if (!f8_overrides_ok(c)) return ATTN_RES_EINVAL;
   if (T == 0 || F == 0) return ATTN_RES_OK;
   attn_res_status_t st = check_matrix(*x);
   for (const attn_res_f8_t* q : {gate, up, h, save_g, save_u})
@@ -214,15 +229,10 @@ attn_res_status_t attn_res_f8_gated(const attn_res_f8_t* x, const attn_res_f8_t*
   for (const attn_res_f8_t* q : {h, save_g, save_u}) spans.add(q, true);
   spans.add(rows_span(h_rows, T, h_row, F, true));
   if (spans.clash()) return ATTN_RES_EALIAS;
-  F8Call c = {};
   st = current_device(&c.device);
   if (st != ATTN_RES_OK) return st;
   cudaError_t e = device_status_word(c.device, &c.err);
   if (e != cudaSuccess) return launched(e);
-  c.a = x;
-  c.w = gate;
-  c.w2 = up;
-  c.gated = true;
   c.activation = activation;
   c.h = h;
   c.g = save_g;

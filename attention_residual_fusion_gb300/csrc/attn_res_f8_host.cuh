@@ -18,10 +18,13 @@ struct F8Call {
   int64_t out_row;
   int out_type;
   bool pdl;
+  int kernel, split;  // overrides, 0 automatic
   int device;
   unsigned* err;
   cudaStream_t stream;
 };
 cudaError_t launch_f8_product(const F8Call& c);
+// Whether the overrides can be met.
+bool f8_overrides_ok(const F8Call& c);
 
 }  // namespace attn_res_host

@@ -62,6 +62,18 @@ struct Attributes {
   Attributes(const Attributes&) = delete;
 };
 
+// The operands' maps, boxes of `a_rows` and 128 rows.
+cudaError_t product_maps(const F8Call& c, uint32_t a_rows, F8ProductMaps* maps) {
+  cudaError_t e = cudaSuccess;
+  for (int t = 0; t < 2; ++t) {
+    const attn_res_f8_t *a = t ? c.a2 : c.a, *w = t ? c.w2 : c.w;
+    // (a term of width 0 has no blocks, and maps of nothing are none)
+    if (e == cudaSuccess && a != nullptr && a->cols > 0) e = codes_map(*a, a_rows, &maps->a[t]);
+    if (e == cudaSuccess && w != nullptr && w->cols > 0) e = codes_map(*w, 128, &maps->w[t]);
+  }
+  return e;
+}
+
 template <int OUT, int ACT, bool ROWS_W>
 struct Wide {
   using C = F8WideCfg;
@@ -85,13 +97,7 @@ struct Wide {
     int pairs;
     cudaError_t e = resident(c, &pairs);
     F8ProductMaps maps = {};
-    auto operands = [&](int t, const attn_res_f8_t* a, const attn_res_f8_t* w) {
-      // (a term of width 0 has no blocks, and maps of nothing are none)
-      if (e == cudaSuccess && a != nullptr && a->cols > 0) e = codes_map(*a, 128, &maps.a[t]);
-      if (e == cudaSuccess && w != nullptr && w->cols > 0) e = codes_map(*w, 128, &maps.w[t]);
-    };
-    operands(0, c.a, c.w);
-    operands(1, c.a2, c.w2);
+    if (e == cudaSuccess) e = product_maps(c, 128, &maps);
     if (e != cudaSuccess) return e;
     const int64_t columns = c.gated ? 128 : C::TN;
     const int64_t m_tiles = (c.a->rows + C::TM - 1) / C::TM, n_tiles = (c.w->rows + columns - 1) / columns;
@@ -103,16 +109,102 @@ struct Wide {
   }
 };
 
+template <int TN, bool GATED, bool ROWS_W>
+cudaError_t launch_narrow(const F8Call& c, int split) {
+  using C = F8NarrowCfg<TN, GATED, ROWS_W>;
+  const auto kern = attn_res_f8_narrow_kernel<TN, GATED, ROWS_W>;
+  static std::atomic<uint64_t> enabled{0};
+  cudaError_t e = allow_smem(kern, C::SMEM, c.device, enabled);
+  F8ProductMaps maps = {};
+  if (e == cudaSuccess) e = product_maps(c, TN, &maps);
+  if (e != cudaSuccess) return e;
+  const int64_t n_tiles = (c.w->rows + 127) / 128, m_tiles = (c.a->rows + TN - 1) / TN;
+  Attributes l(dim3((unsigned)(n_tiles * split), (unsigned)m_tiles, 1), C::THREADS, C::SMEM, (unsigned)split, c.stream);
+  return cudaLaunchKernelEx(&l.cfg, kern, params(c), c.out_type, c.activation, c.pdl, maps);
+}
+
+int64_t k_blocks(const F8Call& c) { return f8_blocks(c.a->cols) + (c.a2 != nullptr ? f8_blocks(c.a2->cols) : 0); }
+// Tokens of a narrow tile.
+int tile_tokens(const F8Call& c) {
+  const int most = c.gated ? 64 : 128;
+  for (int t = 16; t < most; t *= 2)
+    if (c.a->rows <= t) return t;
+  return most;
+}
+
+// The choice of form and split: each one's time by a model of it, in units of 10
+// ns.  Narrow: waves of clusters, kClusters[s] of s CTAs of which the 152 SMs
+// hold at once, two CTAs an SM.
+constexpr int kSms = 152;
+constexpr int kClusters[kF8MaxSplit + 1] = {0, 304, 152, 97, 74, 58, 46, 39, 36};
+int64_t narrow_cost(const F8Call& c, int64_t tiles, int64_t blocks, int tokens, int split) {
+  const int64_t per_cta = (blocks + split - 1) / split, clusters = kClusters[split];
+  const int64_t waves = (tiles + clusters - 1) / clusters;
+  const bool two = (tiles - (waves - 1) * clusters) * split > kSms;
+  const int work = c.gated ? 2 : 1;
+  const int64_t block = (two ? 46 : 28) * work + (tokens > 64 || (c.gated && tokens > 32) ? 24 : 0);
+  return 250 + (waves - 1) * (150 + 46 * work * per_cta) + block * per_cta + (split > 1 ? 60 + 8 * split : 0) + tokens * work;
+}
+int64_t plan_narrow(const F8Call& c, int64_t blocks, int* split) {
+  const int tokens = tile_tokens(c);
+  const int64_t tiles = (c.w->rows + 127) / 128 * ((c.a->rows + tokens - 1) / tokens);
+  int64_t least = narrow_cost(c, tiles, blocks, tokens, 1);
+  *split = 1;
+  for (int s = 2; s <= kF8MaxSplit && s <= blocks; ++s) {
+    const int64_t t = narrow_cost(c, tiles, blocks, tokens, s);
+    if (t < least) {
+      least = t;
+      *split = s;
+    }
+  }
+  return least;
+}
+int64_t wide_cost(const F8Call& c, int64_t blocks) {
+  const int64_t columns = c.gated ? 128 : 256;
+  const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + columns - 1) / columns);
+  return 350 + (tiles + 75) / 76 * (150 + 48 * blocks);
+}
+
+// Token tiles of the narrow form's grid (its y).
+int64_t narrow_max_rows(const F8Call& c) { return int64_t(65535) * (c.gated ? 64 : 128); }
+
+template <bool GATED, bool ROWS_W>
+cudaError_t launch_narrow(const F8Call& c, int split) {
+  switch (tile_tokens(c)) {
+    case 16: return launch_narrow<16, GATED, ROWS_W>(c, split);
+    case 32: return launch_narrow<32, GATED, ROWS_W>(c, split);
+    case 64: return launch_narrow<64, GATED, ROWS_W>(c, split);
+    default:
+      if constexpr (GATED) return cudaErrorInvalidValue;
+      else return launch_narrow<128, GATED, ROWS_W>(c, split);
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_f8_product(const F8Call& c) {
+bool f8_overrides_ok(const F8Call& c) {
+  if (c.kernel < 0 || c.kernel > ATTN_RES_F8_WIDE) return false;
+  if (c.kernel != ATTN_RES_F8_NARROW) return c.split == 0;
+  return c.a->rows <= narrow_max_rows(c) && c.split <= kF8MaxSplit && (c.split <= 1 || c.split <= k_blocks(c));
+}
+
+cudaError_t launch_f8_product(const F8Call& call) {
+  F8Call c = call;
+  const bool rows = c.w->block == ATTN_RES_F8_ROWS;
+  if (c.kernel != ATTN_RES_F8_WIDE && c.split == 0 && c.a->rows <= narrow_max_rows(c)) {
+    const int64_t blocks = k_blocks(c), narrow = plan_narrow(c, blocks, &c.split);
+    if (c.kernel == 0 && narrow <= wide_cost(c, blocks)) c.kernel = ATTN_RES_F8_NARROW;
+  }
+  if (c.kernel == ATTN_RES_F8_NARROW) {
+    if (c.gated) return launch_narrow<true, false>(c, c.split);
+    return rows ? launch_narrow<false, true>(c, c.split) : launch_narrow<false, false>(c, c.split);
+  }
   if (c.gated) {
     const bool silu = c.activation == ATTN_RES_SILU;
     if (c.out == nullptr)
       return silu ? Wide<kF8GatedCodes, ATTN_RES_SILU, false>::launch(c) : Wide<kF8GatedCodes, ATTN_RES_GELU, false>::launch(c);
     return silu ? Wide<kF8GatedBf16, ATTN_RES_SILU, false>::launch(c) : Wide<kF8GatedBf16, ATTN_RES_GELU, false>::launch(c);
   }
-  const bool rows = c.w->block == ATTN_RES_F8_ROWS;
   if (c.out_type == ATTN_RES_OUT_BF16)
     return rows ? Wide<kF8OutBf16, 0, true>::launch(c) : Wide<kF8OutBf16, 0, false>::launch(c);
   return rows ? Wide<kF8OutF32, 0, true>::launch(c) : Wide<kF8OutF32, 0, false>::launch(c);

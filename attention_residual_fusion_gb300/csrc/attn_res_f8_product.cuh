@@ -542,4 +542,353 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
   }
 }
 
+// ---- few tokens: weight rows on the instruction's M side, K split over a cluster -----------
+//
+// A CTA makes a part of the sums of 128 output columns (weight rows, the
+// instruction's M; gated: 128 of the gate and the same 128 of the
+// up-projection) for TN tokens (its N): the part of its range of K.  The CTAs of
+// a cluster share one tile and split K evenly.  Two CTAs an SM, whose first
+// warpgroup loads, issues and makes scales; a thread of the second holds the
+// sums of its weight row, TN (gated 2 TN) of them, each block of K's scaled and
+// added as above.  Then the parts meet in shared memory (over the stages, which
+// are done with), a row of 128 floats for each token, and every CTA adds up and
+// stores a share of the tokens, a warp a token: the gated block's scale of a
+// token's 128 values is then one warp's maximum.
+constexpr int kF8MaxSplit = 8;
+
+template <int TN, bool GATED, bool ROWS_W>
+struct F8NarrowCfg {
+  static constexpr int WT = GATED ? 2 : 1;  // weight tiles
+  static constexpr uint32_t W_BYTES = 128 * 128 * WT, A_BYTES = TN * 128, STAGE = W_BYTES + A_BYTES;
+  // scales of four blocks: TN products with the block's (gated: gate's, then
+  // up's); ROWS_W: the TN tokens' scales and the 128 weight rows'
+  static constexpr int GROUP = 4, SF_RING = 2;
+  static constexpr uint32_t SF_BLOCK = (ROWS_W ? TN + 128 : WT * TN) * 4, SF_BYTES = GROUP * SF_BLOCK;
+  static constexpr int STAGES_FIT = (112 * 1024 - 1024 - SF_RING * (int)SF_BYTES) / (int)STAGE;
+  static constexpr int STAGES = STAGES_FIT < 6 ? STAGES_FIT : 6;
+  static constexpr uint32_t SMEM = STAGES * STAGE + SF_RING * SF_BYTES + 1024;
+  static constexpr int ACC_COLS = WT * TN;
+  static constexpr int COLS = pow2_at_least(2 * ACC_COLS < 32 ? 32 : 2 * ACC_COLS);
+  static constexpr int THREADS = 256;
+  static constexpr int REGS_FEW = 40, REGS_MANY = 208;
+  static_assert(128 * (REGS_FEW + REGS_MANY) <= 128 * THREADS, "the split of the registers");
+  static_assert(STAGES >= 2 && COLS <= 256 && SMEM <= 113 * 1024, "two CTAs an SM");
+  static_assert(STAGES * STAGE >= WT * TN * 128 * 4, "the parts fit over the stages");
+  static_assert(WT * TN <= 128, "sums in registers");
+};
+
+// Four neighbouring columns of a token's row, from column n on.
+__device__ __forceinline__ void store_four(const F8ProductParams& p, int out_type, int64_t m, int64_t n, const float4& x) {
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  if (out_type == ATTN_RES_OUT_BF16) {
+    uint16_t* const o = static_cast<uint16_t*>(p.out) + m * p.out_row + n;
+    const uint32_t lo = pack_bf16x2(x.x, x.y), hi = pack_bf16x2(x.z, x.w);
+    if (n + 4 <= p.n) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (n + e < p.n) o[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e % 2)));
+    }
+  } else {
+    float* const o = static_cast<float*>(p.out) + m * p.out_row + n;
+    if (n + 4 <= p.n) {
+      float4 y = x;
+      if (p.add) {
+        const float4 b = *reinterpret_cast<const float4*>(o);
+        y = make_float4(x.x + b.x, x.y + b.y, x.z + b.z, x.w + b.w);
+      }
+      *reinterpret_cast<float4*>(o) = y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (n + e < p.n) o[e] = v[e] + (p.add ? o[e] : 0.f);
+    }
+  }
+}
+// The same in codes; the warp's lanes hold all 128 columns from n - 4 lane on.
+__device__ __forceinline__ void store_four_codes(const F8View& q, int64_t m, int64_t n, const float4& x) {
+  const uint32_t am = max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w)));
+  const F8Scale s = f8_scale(__reduce_max_sync(0xffffffffu, am));
+  if (n % kF8Block == 0) q.scales[n / kF8Block * q.scales_row + m] = s.by;
+  const uint32_t c = f8_codes(f2_make(x.x, x.y), f2_make(x.z, x.w), s);
+  uint8_t* const o = q.data + m * q.row_bytes + n;
+  if (n + 4 <= q.cols) {
+    *reinterpret_cast<uint32_t*>(o) = c;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (n + e < q.cols) o[e] = (uint8_t)(c >> (8 * e));
+  }
+}
+
+template <int TN, bool GATED, bool ROWS_W>
+__global__ void __launch_bounds__(256, 2)
+    attn_res_f8_narrow_kernel(const __grid_constant__ F8ProductParams p, const int out_type, const int act,
+                              const bool early_weights, const __grid_constant__ F8ProductMaps maps) {
+  using C = F8NarrowCfg<TN, GATED, ROWS_W>;
+  constexpr int S = C::STAGES, R = C::SF_RING, WT = C::WT;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) unsigned long long bars[2 * S + 4 + 2 * R];
+  __shared__ uint32_t tmem_slot;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), split = (int)cluster_nctarank();
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * S, acc_full = empty + 8 * S, acc_empty = acc_full + 16,
+                 sf_full = acc_empty + 16, sf_empty = sf_full + 8 * R;
+  const uint32_t w_at = base, a_at = base + S * C::W_BYTES, sf_at = base + S * C::STAGE;
+  const int n0 = (int)(blockIdx.x / split) * 128, m0 = (int)blockIdx.y * TN;
+  const int blocks0 = p.blocks[0], all_blocks = blocks0 + p.blocks[1];
+  const int k0 = (int)((int64_t)all_blocks * rank / split);
+  const int blocks = (int)((int64_t)all_blocks * (rank + 1) / split) - k0;
+  const int ahead = blocks < S ? blocks : S;
+  bool failed = false;
+
+  auto load_w = [&](int i, int s) {
+    const int k = k0 + i, t = k < blocks0 ? 0 : 1, kb = k < blocks0 ? k : k - blocks0;
+    const uint32_t bar = full + 8 * s;
+    mbar_arrive_expect_tx(bar, C::STAGE);
+    tma_load_2d(w_at + s * C::W_BYTES, &maps.w[GATED ? 0 : t], kb * 128, n0, bar);
+    if constexpr (GATED) tma_load_2d(w_at + s * C::W_BYTES + 128 * 128, &maps.w[1], kb * 128, n0, bar);
+  };
+  auto load_a = [&](int i, int s) {
+    const int k = k0 + i, t = k < blocks0 ? 0 : 1, kb = k < blocks0 ? k : k - blocks0;
+    tma_load_2d(a_at + s * C::A_BYTES, &maps.a[t], kb * 128, m0, full + 8 * s);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * S + 2; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(acc_empty + 8 * i, 4);
+    for (int i = 0; i < R; ++i) {
+      mbar_init(sf_full + 8 * i, 1);
+      mbar_init(sf_empty + 8 * i, 4);
+    }
+    fence_mbar_init();
+    // with ATTN_RES_FLAG_PDL the weights do not depend on the preceding kernel:
+    // the first stages' are on their way before the wait for it
+    if (early_weights)
+      for (int i = 0; i < ahead; ++i) load_w(i, i);
+  }
+  grid_dep_wait();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < ahead; ++i) {
+      if (!early_weights) load_w(i, i);
+      load_a(i, i);
+    }
+  // (TMEM only now: while the preceding kernel runs it may need it itself)
+  if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), C::COLS);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);  // uniform for the compiler
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_FEW));
+    if (warp == 0 && lane == 0) {
+      int issued = ahead;
+      for (int i = ahead; i < blocks; ++i) {
+        const int s = i % S;
+        phase_or_flag(empty + 8 * s, (i / S - 1) & 1, failed, p.err, kErrStageTimeout);
+        if (failed) break;
+        load_w(i, s);
+        load_a(i, s);
+        issued = i + 1;
+      }
+      if (failed)  // copies still in flight land before the CTA ends
+        for (int i = issued > S ? issued - S : 0; i < issued; ++i) (void)phase_wait(full + 8 * (i % S), (i / S) & 1);
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = f8_idesc(128, TN);
+      const bool issuer = elect_one();
+      const uint32_t w_lo = desc_lo(w_at), a_lo = desc_lo(a_at);
+      for (int i = 0; i < blocks; ++i) {
+        const int s = i % S, acc = i & 1;
+        phase_or_flag(full + 8 * s, (i / S) & 1, failed, p.err, kErrStageTimeout);
+        if (i >= 2) phase_or_flag(acc_empty + 8 * acc, ((i >> 1) - 1) & 1, failed, p.err, kErrStageTimeout);
+        failed = __any_sync(0xffffffffu, failed);
+        if (failed) {
+          drain_stages<S>(full, s, i / S);
+          break;
+        }
+        tmem_fence_after();
+        if (issuer) {
+#pragma unroll
+          for (int t = 0; t < WT; ++t)
+            f8_block<1>(tmem + acc * C::ACC_COLS + t * TN, w_lo + (s * C::W_BYTES + t * 128 * 128 >> 4),
+                        a_lo + s * (C::A_BYTES >> 4), idesc);
+          mma_commit<1>(acc_full + 8 * acc);
+          mma_commit<1>(empty + 8 * s);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 2) {
+      for (int k4 = 0, group = 0; k4 < blocks; k4 += C::GROUP, ++group) {
+        const uint32_t r = group % R, slot = sf_at + r * C::SF_BYTES;
+        // (a lane's tokens of a block, and four weight rows)
+        constexpr int PER = (TN + 31) / 32;
+        float v[C::GROUP][PER], w[C::GROUP][ROWS_W ? 4 : WT];
+#pragma unroll
+        for (int j = 0; j < C::GROUP; ++j) {
+          const int k = k0 + k4 + j;
+          const bool one = k < blocks0, in = k4 + j < blocks;
+          const int64_t kb = one ? k : k - blocks0;
+          const F8Scales& sa = p.a[one ? 0 : 1];
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const int64_t m = m0 + 32 * e + lane;
+            v[j][e] = in && m < p.m ? sa.at[kb * sa.row + m] : 1.f;
+          }
+          if constexpr (ROWS_W) {
+            const F8Scales& sw = p.w[one ? 0 : 1];
+            ld_scales4(sw.at + kb * sw.row, n0 + 4 * lane, in ? p.n : 0, w[j]);
+          } else {
+#pragma unroll
+            for (int t = 0; t < WT; ++t) {
+              const F8Scales& sw = p.w[GATED ? t : one ? 0 : 1];
+              w[j][t] = in ? sw.at[n0 / 128 * sw.row + kb] : 1.f;
+            }
+          }
+        }
+        if (group >= R) phase_or_flag(sf_empty + 8 * r, (group / R - 1) & 1, failed, p.err, kErrStageTimeout);
+        failed = __any_sync(0xffffffffu, failed);
+        if (failed) break;
+#pragma unroll
+        for (int j = 0; j < C::GROUP; ++j) {
+          const uint32_t at = slot + j * C::SF_BLOCK;
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            if (32 * e + lane < TN) {
+#pragma unroll
+              for (int t = 0; t < WT; ++t)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * (t * TN + 32 * e + lane)),
+                             "f"(ROWS_W ? v[j][e] : v[j][e] * w[j][ROWS_W ? 0 : t])
+                             : "memory");
+            }
+          if constexpr (ROWS_W) st_shared4(at + 4 * TN + 16 * lane, w[j][0], w[j][1], w[j][2], w[j][3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sf_full + 8 * r);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MANY));
+    const int q = warp % 4;  // warp w reads the TMEM lanes 32 (w % 4) .., that is the weight rows n0 + those
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    constexpr int CH = TN >= 32 ? 32 : 16, PIECES = C::ACC_COLS / CH;  // columns at a time
+    f32x2 sum[C::ACC_COLS / 2];
+#pragma unroll
+    for (int e = 0; e < C::ACC_COLS / 2; ++e) sum[e] = f2_make(0.f, 0.f);
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (phase_done(bar, parity) || failed) return;
+      if (!phase_wait(bar, parity)) {
+        failed = true;
+        atomicOr(p.err, kErrStageTimeout);
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < blocks; ++i) {
+      const int acc = i & 1, group = i / C::GROUP, in_group = i % C::GROUP, r = group % R;
+      if (in_group == 0) wait(sf_full + 8 * r, (group / R) & 1);
+      const uint32_t at = sf_at + r * C::SF_BYTES + in_group * C::SF_BLOCK;
+      float mine = 1.f;  // ROWS_W: this weight row's scale
+      if constexpr (ROWS_W) mine = ld_shared(at + 4 * (TN + 32 * q + lane));
+      wait(acc_full + 8 * acc, (i >> 1) & 1);
+      __syncwarp();
+      tmem_fence_after();
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c) {
+        uint32_t v[CH];
+        tmem_ld(lanes + acc * C::ACC_COLS + CH * c, v);
+        tmem_ld_wait(v);
+        if (c == PIECES - 1) {
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + 8 * acc);
+        }
+#pragma unroll
+        for (int e = 0; e < CH / 2; e += 2) {
+          f32x2 s[2];
+          ld_shared_pairs(at + 4 * (CH * c + 2 * e), s);
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const f32x2 x = f2_make(__uint_as_float(v[2 * (e + o)]), __uint_as_float(v[2 * (e + o) + 1]));
+            f32x2& to = sum[CH / 2 * c + e + o];
+            to = f2_fma(x, ROWS_W ? f2_mul(s[o], f2_make(mine, mine)) : s[o], to);
+          }
+        }
+      }
+      if (in_group == C::GROUP - 1 || i == blocks - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sf_empty + 8 * r);
+      }
+    }
+    failed = __any_sync(0xffffffffu, failed);
+    grid_dep_launch_dependents();
+    // The parts, over the stages: every product that read these is complete, and
+    // so is every copy into them (unless a wait has given up).
+    if (!failed) {
+#pragma unroll
+      for (int e = 0; e < C::ACC_COLS; ++e)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + 4 * (128 * e + 32 * q + lane)),
+                     "f"(e % 2 ? f2_hi(sum[e / 2]) : f2_lo(sum[e / 2]))
+                     : "memory");
+    }
+    __syncwarp();
+    if (split > 1) cluster_sync();
+    else asm volatile("bar.sync 1, 128;" ::: "memory");
+    const int64_t left = p.m - m0;
+    const int tokens = left < TN ? (int)left : TN;
+    const int64_t n = n0 + 4 * lane;
+#pragma unroll 1
+    for (int t = rank * 4 + q; t < tokens; t += split * 4) {
+      float4 x[WT];
+#pragma unroll
+      for (int y = 0; y < WT; ++y) {
+        const uint32_t at = base + 4 * (128 * (TN * y + t) + 4 * lane);
+        float4 part[kF8MaxSplit];  // the loads of all parts together; added in the ranks' order
+#pragma unroll
+        for (int k = 0; k < kF8MaxSplit; ++k)
+          if (k < split)
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(part[k].x), "=f"(part[k].y), "=f"(part[k].z), "=f"(part[k].w)
+                         : "r"(map_rank(at, (uint32_t)k))
+                         : "memory");
+        x[y] = part[0];
+#pragma unroll
+        for (int k = 1; k < kF8MaxSplit; ++k)
+          if (k < split)
+            x[y] = make_float4(x[y].x + part[k].x, x[y].y + part[k].y, x[y].z + part[k].z, x[y].w + part[k].w);
+      }
+      if (failed) continue;
+      const int64_t m = m0 + t;
+      if constexpr (!GATED) {
+        store_four(p, out_type, m, n, x[0]);
+      } else {
+        if (p.g.data) store_four_codes(p.g, m, n, x[0]);
+        if (p.u.data) store_four_codes(p.u, m, n, x[WT - 1]);
+        auto one = [&](float g, float u) {
+          return (act == ATTN_RES_SILU ? f8_act<ATTN_RES_SILU>(g) : f8_act<ATTN_RES_GELU>(g)) * u;
+        };
+        const float4& u = x[WT - 1];
+        const float4 h = make_float4(one(x[0].x, u.x), one(x[0].y, u.y), one(x[0].z, u.z), one(x[0].w, u.w));
+        if (p.h.data) store_four_codes(p.h, m, n, h);
+        else store_four(p, ATTN_RES_OUT_BF16, m, n, h);
+      }
+    }
+  }
+  __syncwarp();
+  if (warp < 4 && split > 1) cluster_sync();  // (the parts' way, which the other four go)
+  // No CTA ends while its parts are being read: every load's value has been used
+  // by then, so the arrival orders nothing.
+  __syncwarp();
+  if (split > 1) cluster_arrive_relaxed();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    tmem_free<1>(tmem, C::COLS);
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_wait_acquire();
+  }
+}
+
 }  // namespace attn_res_dev

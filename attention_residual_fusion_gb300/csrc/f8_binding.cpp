@@ -107,6 +107,11 @@ std::vector<py::object> outputs(const char* name, const py::object& given, size_
   return v;
 }
 
+uint32_t flags_of(bool pdl, int kernel, int split) {
+  if (kernel < 0 || kernel > 15 || split < 0 || split > 255) refuse("no such kernel or split");
+  return attn_res_binding::flags_of(pdl) | ATTN_RES_FLAG_KERNEL(kernel) | ATTN_RES_FLAG_SPLIT(split);
+}
+
 int activation_code(const std::string& a) {
   if (a == "silu") return ATTN_RES_SILU;
   if (a == "gelu") return ATTN_RES_GELU;
@@ -126,11 +131,11 @@ py::object quantize(const at::Tensor& x, int block, const py::object& out, const
   const On on(x.device(), stream);
   const Result q("out", out, rows, cols, block, x.device());
   if (!wanted(transposed)) {
-    check(attn_res_f8_quantize(bf16("x", x), row_stride(x, 8), &q.c, nullptr, flags_of(pdl), on.handle));
+    check(attn_res_f8_quantize(bf16("x", x), row_stride(x, 8), &q.c, nullptr, attn_res_binding::flags_of(pdl), on.handle));
     return q.object;
   }
   const Result t("transposed", transposed, cols, rows, block, x.device());
-  check(attn_res_f8_quantize(bf16("x", x), row_stride(x, 8), &q.c, &t.c, flags_of(pdl), on.handle));
+  check(attn_res_f8_quantize(bf16("x", x), row_stride(x, 8), &q.c, &t.c, attn_res_binding::flags_of(pdl), on.handle));
   return py::make_tuple(q.object, t.object);
 }
 
@@ -139,12 +144,13 @@ at::Tensor dequantize(const F8Tensor& q, const OptTensor& out, bool pdl, const p
   const On on(q.device(), stream);
   if (out) check_rows("out", *out, c.rows, c.cols, q.device());
   const at::Tensor x = out ? *out : padded(c.rows, c.cols, 8, at::kBFloat16, q.device());
-  check(attn_res_f8_dequantize(&c, bf16("out", x), row_stride(x, 8), flags_of(pdl), on.handle));
+  check(attn_res_f8_dequantize(&c, bf16("out", x), row_stride(x, 8), attn_res_binding::flags_of(pdl), on.handle));
   return x;
 }
 
 at::Tensor matmul(const F8Tensor& a, const F8Tensor& w, const OptTensor& out, const py::object& dtype, bool add,
-                  const std::optional<std::tuple<F8Tensor, F8Tensor>>& plus, bool pdl, const py::object& stream) {
+                  const std::optional<std::tuple<F8Tensor, F8Tensor>>& plus, bool pdl, int kernel, int split,
+                  const py::object& stream) {
   const at::Device device = a.device();
   same_device(device, w);
   const attn_res_f8_t ca = a.matrix(), cw = w.matrix();
@@ -181,13 +187,13 @@ at::Tensor matmul(const F8Tensor& a, const F8Tensor& w, const OptTensor& out, co
   }
   check(attn_res_f8_matmul(&ca, &cw, plus ? &ca2 : nullptr, plus ? &cw2 : nullptr, address("out", y), row_stride(y, to),
                            type == at::kBFloat16 ? ATTN_RES_OUT_BF16 : add ? ATTN_RES_OUT_F32_ADD : ATTN_RES_OUT_F32,
-                           flags_of(pdl), on.handle));
+                           flags_of(pdl, kernel, split), on.handle));
   return y;
 }
 
 py::object gated(const F8Tensor& x, const F8Tensor& gate, const F8Tensor& up, const std::string& activation,
                  const py::object& out, const py::object& dtype, const py::object& save, bool pdl,
-                 const py::object& stream) {
+                 int kernel, int split, const py::object& stream) {
   const at::Device device = x.device();
   same_device(device, gate);
   same_device(device, up);
@@ -230,8 +236,8 @@ py::object gated(const F8Tensor& x, const F8Tensor& gate, const F8Tensor& up, co
     u.emplace("save", into[1], T, F, ATTN_RES_F8_ROWS, device);
   }
   check(attn_res_f8_gated(&cx, &cg, &cu, act, codes ? &h->c : nullptr, codes ? nullptr : bf16("out", rows),
-                          codes ? 0 : row_stride(rows, 8), g ? &g->c : nullptr, u ? &u->c : nullptr, flags_of(pdl),
-                          on.handle));
+                          codes ? 0 : row_stride(rows, 8), g ? &g->c : nullptr, u ? &u->c : nullptr,
+                          flags_of(pdl, kernel, split), on.handle));
   if (!g) return result;
   return py::make_tuple(result, g->object, u->object);
 }
@@ -254,7 +260,7 @@ py::object gated_backward(const at::Tensor& dh, const F8Tensor& gate, const F8Te
     r.emplace_back("out", into[i], i < 2 ? T : F, i < 2 ? F : T, ATTN_RES_F8_ROWS, device);
   check(attn_res_f8_gated_backward(bf16("dh", dh), row_stride(dh, 8), &cg, &cu, act, &r[0].c, &r[1].c,
                                    transposed ? &r[2].c : nullptr, transposed ? &r[3].c : nullptr,
-                                   transposed ? &r[4].c : nullptr, flags_of(pdl), on.handle));
+                                   transposed ? &r[4].c : nullptr, attn_res_binding::flags_of(pdl), on.handle));
   py::tuple t(r.size());
   for (size_t i = 0; i < r.size(); ++i) t[i] = r[i].object;
   return t;
@@ -298,13 +304,15 @@ matrix, quantised by itself: (q, qt).)");
   m.def("dequantize", &dequantize, "q"_a, "out"_a = py::none(), py::kw_only(), "pdl"_a = false,
         "stream"_a = py::none(), "The bf16 values that ``q`` stands for (attn_res_f8_dequantize).");
   m.def("matmul", &matmul, "a"_a, "w"_a, "out"_a = py::none(), py::kw_only(), "dtype"_a = py::none(), "add"_a = false,
-        "plus"_a = py::none(), "pdl"_a = false, "stream"_a = py::none(),
+        "plus"_a = py::none(), "pdl"_a = false, "kernel"_a = 0, "split"_a = 0, "stream"_a = py::none(),
         R"(``a`` [m, k] (block 1) times the transpose of ``w`` [n, k] (either block), plus
 the product of the pair ``plus`` if given: [m, n] in ``dtype``, bfloat16 (the
 default) or float32, fp32 sums (attn_res_f8_matmul).  ``add`` adds to the float32
-``out``.)");
+``out``.  ``kernel`` (KERNEL_NARROW, KERNEL_WIDE) and ``split`` override the
+automatic choice.)");
   m.def("gated", &gated, "x"_a, "gate"_a, "up"_a, "activation"_a = "silu", "out"_a = py::none(), py::kw_only(),
-        "dtype"_a = py::none(), "save"_a = false, "pdl"_a = false, "stream"_a = py::none(),
+        "dtype"_a = py::none(), "save"_a = false, "pdl"_a = false, "kernel"_a = 0, "split"_a = 0,
+        "stream"_a = py::none(),
         R"(act(x gate^T) * (x up^T) for x [T, H] (block 1), gate and up [F, H] (block 128):
 [T, F] as an F8Tensor, or with ``dtype`` (or ``out``) bfloat16 as a tensor
 (attn_res_f8_gated).  ``save`` (True, or two F8Tensors to fill) keeps both

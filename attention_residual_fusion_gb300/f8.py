@@ -31,6 +31,8 @@ import threading
 from . import _build, load_binding
 
 BLOCK = 128
+# Forms of the products (kernel=; 0: automatic), see attn_res_f8_matmul.
+KERNEL_NARROW, KERNEL_WIDE = 1, 2
 _CALLS = ("F8Tensor", "quantize", "dequantize", "matmul", "gated", "gated_backward")
 _loading = threading.Lock()
 

@@ -525,7 +525,21 @@ attn_res_status_t attn_res_f8_dequantize(const attn_res_f8_t* q, attn_res_bf16_t
  * out_type: ATTN_RES_OUT_BF16, ATTN_RES_OUT_F32, or ATTN_RES_OUT_F32_ADD, which
  * adds to the fp32 rows that are there.  fp32 rows: 16-byte aligned, out_row a
  * multiple of 4.  A width of 0 makes zeros.
+ *
+ * ATTN_RES_FLAG_PDL lets the narrow form read w and w2 before the preceding
+ * kernel is complete (the contract of that flag, with them in the place of the
+ * bank rows); elsewhere it does nothing.  Beside it, flags takes tuning overrides
+ * (0 = automatic; the results do not depend on them beyond fp32 summation order):
+ *   KERNEL(k): ATTN_RES_F8_NARROW -- a CTA for 128 rows of w and up to 128 of a
+ *              (the gated block: 64), K split over a cluster;
+ *              ATTN_RES_F8_WIDE -- persistent CTA pairs, 256 rows of a and 256
+ *              of w at a time;
+ *   SPLIT(s):  with ATTN_RES_F8_NARROW, the CTAs that share a tile's K: 1..8, at
+ *              most the 128-column blocks of K.
+ * An override that cannot be met is ATTN_RES_EINVAL.
  */
+#define ATTN_RES_F8_NARROW 1
+#define ATTN_RES_F8_WIDE 2
 #define ATTN_RES_OUT_BF16 0
 #define ATTN_RES_OUT_F32 1
 #define ATTN_RES_OUT_F32_ADD 2

@@ -166,47 +166,64 @@ def product_want(pairs, cols):
     return want, R.product_bound(mag, cols)
 
 
+# the forms of a product, the narrow one with K split over clusters of several sizes
+FORMS = [dict(kernel=f8.KERNEL_WIDE)] + [dict(kernel=f8.KERNEL_NARROW, split=s) for s in (1, 2, 3, 5, 8)] + [dict()]
+
+
+def form(kw, k):
+    """The override as far as K's blocks allow."""
+    return {**kw, "split": min(kw["split"], max(1, R.blocks(k)))} if "split" in kw else kw
+
+
+@pytest.mark.parametrize("kw", FORMS, ids=lambda kw: "-".join(f"{a}{b}" for a, b in kw.items()) or "auto")
 @pytest.mark.parametrize("block", [1, 128])
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
-def test_matmul(m, n, k, block):
+def test_matmul(m, n, k, block, kw):
+    kw = form(kw, k)
     a, w = quantized(m, k, 1), quantized(n, k, 2, block, scale=0.02)
     want, bound = product_want([(a, w)], k)
     out = Rows(m, n, 8)
-    f8.matmul(a.t, w.t, out.t)
+    f8.matmul(a.t, w.t, out.t, **kw)
     within(out.t, want, bound + BF16_HALF * (want.abs() + bound), "bf16")
     assert out.intact() and a.intact() and w.intact()
-    f = f8.matmul(a.t, w.t, dtype=torch.float32)
+    f = f8.matmul(a.t, w.t, dtype=torch.float32, **kw)
     assert f.shape == (m, n) and f.dtype == torch.float32
     within(f, want, bound, "fp32")
     # the same bits again, and bf16 is fp32 rounded
-    assert torch.equal(f, f8.matmul(a.t, w.t, dtype=torch.float32))
+    assert torch.equal(f, f8.matmul(a.t, w.t, dtype=torch.float32, **kw))
     assert torch.equal(out.t, f.to(torch.bfloat16))
     # added to what is there: one more rounding
     g = torch.Generator(device="cuda").manual_seed(5)
     before = torch.randn(m, n, generator=g, device="cuda")
     buf = torch.full((m, -(-n // 4) * 4 + 4), 3.25, device="cuda")
     buf[:, :n] = before
-    f8.matmul(a.t, w.t, buf[:, :n], add=True)
+    f8.matmul(a.t, w.t, buf[:, :n], add=True, **kw)
     assert torch.equal(buf[:, :n], before + f)
     assert bool((buf[:, n:] == 3.25).all())
 
 
+@pytest.mark.parametrize("kw", FORMS, ids=str)
 @pytest.mark.parametrize("block", [1, 128])
 @pytest.mark.parametrize("m,n,k,k2", [(1, 200, 256, 100), (40, 300, 129, 513), (300, 520, 1000, 128), (513, 256, 1, 2000)])
-def test_matmul_of_two_pairs(m, n, k, k2, block):
+def test_matmul_of_two_pairs(m, n, k, k2, block, kw):
+    kw = form(kw, 128 * (R.blocks(k) + R.blocks(k2)))
     pairs = [(quantized(m, kk, s), quantized(n, kk, s + 1, block, pad=1, scale=0.05)) for kk, s in ((k, 1), (k2, 3))]
     want, bound = product_want(pairs, k + k2 + 128)
     (a, w), (a2, w2) = pairs
-    f = f8.matmul(a.t, w.t, dtype=torch.float32, plus=(a2.t, w2.t))
+    f = f8.matmul(a.t, w.t, dtype=torch.float32, plus=(a2.t, w2.t), **kw)
     within(f, want, bound)
-    h = f8.matmul(a.t, w.t, plus=(a2.t, w2.t))
+    h = f8.matmul(a.t, w.t, plus=(a2.t, w2.t), **kw)
     assert torch.equal(h, f.to(torch.bfloat16))
 
 
 @pytest.mark.parametrize("block", [1, 128])
 def test_matmul_without_columns(block):
     """A sum over no tokens is zero; behind it a second pair counts alone."""
-    m, n = 130, 300
+    for m, n in ((130, 300), (20, 300)):
+        without_columns(m, n, block)
+
+
+def without_columns(m, n, block):
     a, w = f8.F8Tensor.empty(m, 0), f8.F8Tensor.empty(n, 0, block)
     out = torch.full((m, n), 9.0, device="cuda")
     f8.matmul(a, w, out)
@@ -323,29 +340,32 @@ def check_codes(got, want, error, what):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("kw", FORMS, ids=str)
 @pytest.mark.parametrize("T,F,H", GATED)
-def test_gated(T, F, H, act):
+def test_gated(T, F, H, act, kw):
+    kw = form(kw, H)
     x = quantized(T, H, 1)
     wg, wu = quantized(F, H, 2, 128, scale=H ** -0.5), quantized(F, H, 3, 128, pad=1, scale=H ** -0.5)
     g, u, h, eg, eu, eh = gated_want(x, wg, wu, act)
     out = [Matrix(T, F, 1, i) for i in range(3)]
-    f8.gated(x.t, wg.t, wu.t, act, out[0].t, save=(out[1].t, out[2].t))
+    f8.gated(x.t, wg.t, wu.t, act, out[0].t, save=(out[1].t, out[2].t), **kw)
     for got, want, e, what in zip(out, (h, g, u), (eh, eg, eu), ("h", "g", "u")):
         check_codes(got, want, e, what)
     # without the checkpoint the same h; in bf16 from the same sums
-    again = f8.gated(x.t, wg.t, wu.t, act)
+    again = f8.gated(x.t, wg.t, wu.t, act, **kw)
     assert torch.equal(again.data.view(torch.uint8), out[0].codes) and torch.equal(again.scales, out[0].scales)
     rows = Rows(T, F, 8)
-    f8.gated(x.t, wg.t, wu.t, act, rows.t)
+    f8.gated(x.t, wg.t, wu.t, act, rows.t, **kw)
     within(rows.t, h, eh + BF16_HALF * (h.abs() + eh), "bf16")
     assert rows.intact()
-    b, sg, su = f8.gated(x.t, wg.t, wu.t, act, dtype=torch.bfloat16, save=True)
+    b, sg, su = f8.gated(x.t, wg.t, wu.t, act, dtype=torch.bfloat16, save=True, **kw)
     assert torch.equal(b, rows.t)
     assert torch.equal(sg.data.view(torch.uint8), out[1].codes) and torch.equal(su.scales, out[2].scales)
 
 
+@pytest.mark.parametrize("kw", FORMS[:3], ids=str)
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-def test_gated_of_large_and_special_values(act):
+def test_gated_of_large_and_special_values(act, kw):
     """Projections far beyond the activation's bend, rows of NaN, rows of zeros."""
     T, F, H = 140, 260, 300
     x = quantized(T, H, 1, scale=30.0)
@@ -355,7 +375,7 @@ def test_gated_of_large_and_special_values(act):
     x.scales[:, 11] *= 2.0 ** 40
     wg, wu = quantized(F, H, 2, 128), quantized(F, H, 3, 128)
     out = [Matrix(T, F) for _ in range(3)]
-    f8.gated(x.t, wg.t, wu.t, act, out[0].t, save=(out[1].t, out[2].t))
+    f8.gated(x.t, wg.t, wu.t, act, out[0].t, save=(out[1].t, out[2].t), **kw)
     for o in out:
         assert bool(torch.isnan(o.scales[:, 3]).all()) and bool(torch.isnan(o.scales[:, 7]).all())
         assert bool((o.codes[3] == 0).all())
