@@ -1,4 +1,6 @@
 // attn_res_f8_product.cu -- launches of the 8-bit products.
+#include <algorithm>
+
 #include "attn_res_f8_host.cuh"
 #include "attn_res_f8_product.cuh"
 #include "attn_res_tensor_host.cuh"
@@ -132,18 +134,33 @@ int tile_tokens(const F8Call& c) {
   return most;
 }
 
-// The choice of form and split: each one's time by a model of it, in units of 10
-// ns.  Narrow: waves of clusters, kClusters[s] of s CTAs of which the 152 SMs
-// hold at once, two CTAs an SM.
+// The choice of form and split: each one's time by a model of it, in ns, whose
+// constants were fitted to 618 products (graph replays on GB300, inputs in L2:
+// 1..1024 tokens x 512..16384 columns x 512..7200, gated and not, every split).
+// Over these the choice takes 2 % longer than the best form in the geometric
+// mean, and 28 % at most (512 x 512 x 2048: 7.4 us, 5.8 in eight parts).
+//
+// Narrow: waves of clusters, kClusters[s] of s CTAs of which the 152 SMs hold at
+// once, two CTAs an SM.  A block of K takes as long as its weights' way from L2,
+// or the sums' way through registers, more of either with a second CTA beside.
+//   tokens x columns x K        parts: 1     2     4     5     8    wide   (us)
+//   1 x 7168 x 7168              16.0   9.5   8.6   8.0  10.2   28.4
+//   128 x 7168 x 7168            30.1  18.7  16.2  15.3  21.4   29.8
+//   333 x 2050 x 7200            30.9  19.1  15.8  14.7  19.2   29.6
+//   512 x 16384 x 1024           27.1  36.9  52.0  66.3  93.5   15.3
+//   64 x 4096 x 7168 gated       38.4  22.5  13.8  16.9  14.5   31.2
 constexpr int kSms = 152;
 constexpr int kClusters[kF8MaxSplit + 1] = {0, 304, 152, 97, 74, 58, 46, 39, 36};
 int64_t narrow_cost(const F8Call& c, int64_t tiles, int64_t blocks, int tokens, int split) {
   const int64_t per_cta = (blocks + split - 1) / split, clusters = kClusters[split];
   const int64_t waves = (tiles + clusters - 1) / clusters;
   const bool two = (tiles - (waves - 1) * clusters) * split > kSms;
-  const int work = c.gated ? 2 : 1;
-  const int64_t block = (two ? 46 : 28) * work + (tokens > 64 || (c.gated && tokens > 32) ? 24 : 0);
-  return 250 + (waves - 1) * (150 + 46 * work * per_cta) + block * per_cta + (split > 1 ? 60 + 8 * split : 0) + tokens * work;
+  const int64_t weights = c.gated ? 2 : 1, sums = weights * tokens;
+  const int64_t one_cta = std::max<int64_t>(159 * weights, 141 + 33 * sums / 10);
+  const int64_t two_ctas = std::max<int64_t>(306 * weights, 287 + 48 * sums / 10);
+  int64_t t = 2320 + 21 * sums + (waves - 1) * (4380 + two_ctas * per_cta) + (two ? two_ctas : one_cta) * per_cta;
+  if (split > 1) t += 270 + 13 * split * sums / 10;
+  return t;
 }
 int64_t plan_narrow(const F8Call& c, int64_t blocks, int* split) {
   const int tokens = tile_tokens(c);
@@ -159,10 +176,11 @@ int64_t plan_narrow(const F8Call& c, int64_t blocks, int* split) {
   }
   return least;
 }
+// Wide: waves of pairs.
 int64_t wide_cost(const F8Call& c, int64_t blocks) {
   const int64_t columns = c.gated ? 128 : 256;
   const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + columns - 1) / columns);
-  return 350 + (tiles + 75) / 76 * (150 + 48 * blocks);
+  return 1630 + (tiles + kSms / 2 - 1) / (kSms / 2) * (3190 + (c.w->block == ATTN_RES_F8_ROWS ? 820 : 471) * blocks);
 }
 
 // Token tiles of the narrow form's grid (its y).
