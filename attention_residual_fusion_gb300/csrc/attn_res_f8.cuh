@@ -24,10 +24,19 @@ struct F8View {
 
 __host__ __device__ constexpr int64_t f8_blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
 
-// Bits of |x|: as integers they order like the magnitudes, with every NaN
-// above infinity, so one integer maximum finds a group's amax and whether it
-// holds anything that is no number.
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// max(m, |a|, |b|), a NaN if there is one (its bits are then above infinity's).
+__device__ __forceinline__ float amax3(float m, f32x2 v) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(f2_lo(v)), "f"(f2_hi(v)));
+  return r;
+}
+__device__ __forceinline__ float amax3(float m, float a, float b) { return amax3(m, f2_make(a, b)); }
+__device__ __forceinline__ float warp_amax(float m) {
+  uint32_t r;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=r"(r) : "f"(m));
+  return __uint_as_float(r);
+}
 
 // A group's scale from the bits of its amax, and what its codes are made with:
 // its correctly rounded inverse and whether quotients may be taken with it.
@@ -50,11 +59,11 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t amax) {
 // processor", 1990).  For a scale between 2^-96 and 2^96 nothing over- or
 // underflows on the way that matters: the quotient is 448 at most, and where x
 // is so small that its remainder is lost it is far below half the smallest
-// code.  Negated, because so a zero keeps its sign.
-__device__ __forceinline__ f32x2 f8_negated_quotient2(f32x2 x, float by, float inverse) {
-  const f32x2 r = f2_make(-inverse, -inverse);
-  const f32x2 q = f2_mul(x, r);
-  return f2_fma(f2_fma(q, f2_make(by, by), x), r, q);
+// code; with a smaller scale the remainder may be lost, and the quotient is off
+// by a unit in its last place.  Negated, because so a zero keeps its sign.
+__device__ __forceinline__ f32x2 f8_negated_quotient2(f32x2 x, f32x2 by, f32x2 minus_inverse) {
+  const f32x2 q = f2_mul(x, minus_inverse);
+  return f2_fma(f2_fma(q, by, x), minus_inverse, q);
 }
 __device__ __forceinline__ bool f8_quotients_held(float by) { return by >= 0x1p-96f && by <= 0x1p96f; }
 
@@ -69,15 +78,22 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return w;
 }
-// Codes of four values over one scale.
+// Codes of four values over one scale that is a number.
+__device__ __forceinline__ uint32_t f8_codes(f32x2 lo, f32x2 hi, float by, float inverse) {
+  const f32x2 b = f2_make(by, by), r = f2_make(-inverse, -inverse);
+  const f32x2 x = f8_negated_quotient2(lo, b, r), y = f8_negated_quotient2(hi, b, r);
+  return e4m3x4(f2_lo(x), f2_hi(x), f2_lo(y), f2_hi(y)) ^ 0x80808080u;
+}
+// Over any scale (0 where that is NaN).
 __device__ __forceinline__ uint32_t f8_codes(f32x2 lo, f32x2 hi, const F8Scale& s) {
-  if (f8_quotients_held(s.by)) {
-    const f32x2 a = f8_negated_quotient2(lo, s.by, s.inverse), b = f8_negated_quotient2(hi, s.by, s.inverse);
-    return e4m3x4(f2_lo(a), f2_hi(a), f2_lo(b), f2_hi(b)) ^ 0x80808080u;
-  }
-  if (!(s.by < __int_as_float(0x7f800000))) return 0u;
-  return e4m3x4(__fdiv_rn(f2_lo(lo), s.by), __fdiv_rn(f2_hi(lo), s.by), __fdiv_rn(f2_lo(hi), s.by),
-                __fdiv_rn(f2_hi(hi), s.by));
+  const uint32_t c = f8_codes(lo, hi, s.by, s.inverse);
+  return s.by == s.by ? c : 0u;
+}
+// The same, correctly rounded whatever the scale.
+__device__ __forceinline__ uint32_t f8_codes_far(f32x2 lo, f32x2 hi, float by) {
+  const uint32_t c = e4m3x4(__fdiv_rn(f2_lo(lo), by), __fdiv_rn(f2_hi(lo), by), __fdiv_rn(f2_lo(hi), by),
+                            __fdiv_rn(f2_hi(hi), by));
+  return by == by ? c : 0u;
 }
 // The values of a pair of codes (the low 16 bits), exactly.
 __device__ __forceinline__ f32x2 e4m3_pair(uint32_t codes) {
@@ -107,33 +123,50 @@ __device__ __forceinline__ float f8_sigmoid(float z) {
   asm("rcp.approx.f32 %0, %1;" : "=f"(p) : "f"(1.f + __expf(-z)));
   return p;
 }
+// Of a pair, to a few units of 2^-23: with s = z log2(e) rounded, exp(-z) = 2^-s
+// (1 + d ln 2), d what the rounding of s and of the constant took off.
+__device__ __forceinline__ f32x2 f8_sigmoid2(f32x2 z) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kLog2eRest = (float)(1.4426950408889634073599 - (double)kLog2e), kLn2 = 0.69314718055994531f;
+  z = f2_make(fminf(f2_lo(z), 200.f), fminf(f2_hi(z), 200.f));  // (exp(-z) is 0 there, and d a number)
+  const f32x2 s = f2_mul(z, f2_make(kLog2e, kLog2e));
+  const f32x2 d = f2_fma(z, f2_make(-kLog2eRest, -kLog2eRest), f2_fma(z, f2_make(-kLog2e, -kLog2e), s));
+  float e[2], p[2];
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[0]) : "f"(-f2_lo(s)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[1]) : "f"(-f2_hi(s)));
+  const f32x2 e2 = f2_make(e[0], e[1]), y = f2_fma(e2, f2_mul(d, f2_make(kLn2, kLn2)), e2);
+  // (an infinite e may have made a NaN of it: min then gives infinity)
+  const float inf = __int_as_float(0x7f800000);
+  // a quarter of 1 + e, so that its reciprocal is no subnormal number
+  const f32x2 q = f2_make(0.25f, 0.25f);
+  const f32x2 w = f2_fma(f2_make(fminf(f2_lo(y), inf), fminf(f2_hi(y), inf)), q, q);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p[0]) : "f"(f2_lo(w)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p[1]) : "f"(f2_hi(w)));
+  return f2_mul(f2_make(p[0], p[1]), q);
+}
 
 template <int ACT>
 __device__ __forceinline__ float f8_act(float g) {
   return g * f8_sigmoid(f8_gate_arg<ACT>(g));
 }
-// act(g) and its derivative p + g p (1 - p) z'(g) of a pair.  The derivative is
-// taken of g held to +-100, where it is 1 or 0, so that z' stays a number (at
-// 1e19 0 x inf would come of it).
+// act(g) and its derivative p + g p (1 - p) z'(g) of a pair.  (g^2 in z' is held
+// to 10^4, where p is 1 or 0, so that z' stays a number: at g = 1e19 0 x inf would
+// come of it.)
 template <int ACT>
 __device__ __forceinline__ void f8_act_both2(f32x2 g, f32x2& act, f32x2& slope) {
-  float c[2], p[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float x = e ? f2_hi(g) : f2_lo(g);
-    // (not fminf and fmaxf, which drop a NaN)
-    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, 0f42C80000;\n\tmax.NaN.f32 %0, t, 0fC2C80000;\n\t}" : "=f"(c[e]) : "f"(x));
-    p[e] = f8_sigmoid(f8_gate_arg<ACT>(c[e]));
-  }
-  const f32x2 c2 = f2_make(c[0], c[1]), p2 = f2_make(p[0], p[1]);
-  act = f2_mul(g, p2);
-  const f32x2 minus = f2_make(-1.f, -1.f), one = f2_make(1.f, 1.f);
-  f32x2 t = f2_mul(f2_mul(c2, p2), f2_fma(p2, minus, one));
+  const f32x2 one = f2_make(1.f, 1.f), minus = f2_make(-1.f, -1.f);
+  f32x2 z = g, dz = one;
   if constexpr (ACT != ATTN_RES_SILU) {
-    const float q = 3.f * kGeluCubic * kGeluScale;
-    t = f2_mul(t, f2_fma(f2_mul(c2, f2_make(q, q)), c2, f2_make(kGeluScale, kGeluScale)));
+    const f32x2 k = f2_make(kGeluScale, kGeluScale), kc = f2_make(kGeluScale * kGeluCubic, kGeluScale * kGeluCubic);
+    const f32x2 sq = f2_mul(g, g);
+    z = f2_mul(g, f2_fma(sq, kc, k));
+    const f32x2 held = f2_make(fminf(f2_lo(sq), 1e4f), fminf(f2_hi(sq), 1e4f));
+    dz = f2_fma(held, f2_make(3.f * kGeluScale * kGeluCubic, 3.f * kGeluScale * kGeluCubic), k);
   }
-  slope = f2_fma(t, one, p2);
+  const f32x2 p = f8_sigmoid2(z);
+  act = f2_mul(g, p);
+  f32x2 t = f2_mul(act, f2_fma(p, minus, one));
+  slope = f2_fma(t, dz, p);
 }
 
 }  // namespace attn_res_dev

@@ -205,10 +205,10 @@ __device__ __forceinline__ void store_f32(float* o, const f32x2* v, int left, bo
 template <class Other>
 __device__ __forceinline__ void store_f8(const F8View& q, int64_t row, int64_t col, bool stores, const f32x2* v,
                                          Other other) {
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) m = max(m, max(magnitude(f2_lo(v[k])), magnitude(f2_hi(v[k]))));
-  const F8Scale s = f8_scale(other(m));
+  for (int k = 0; k < 32; ++k) m = amax3(m, v[k]);
+  const F8Scale s = f8_scale(other(__float_as_uint(m)));
   if (!stores || row >= q.rows) return;
   if (col % kF8Block == 0) q.scales[col / kF8Block * q.scales_row + row] = s.by;
   uint8_t* const o = q.data + row * q.row_bytes + col;
@@ -608,8 +608,7 @@ __device__ __forceinline__ void store_four(const F8ProductParams& p, int out_typ
 }
 // The same in codes; the warp's lanes hold all 128 columns from n - 4 lane on.
 __device__ __forceinline__ void store_four_codes(const F8View& q, int64_t m, int64_t n, const float4& x) {
-  const uint32_t am = max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w)));
-  const F8Scale s = f8_scale(__reduce_max_sync(0xffffffffu, am));
+  const F8Scale s = f8_scale(__float_as_uint(warp_amax(amax3(amax3(0.f, x.x, x.y), x.z, x.w))));
   if (n % kF8Block == 0) q.scales[n / kF8Block * q.scales_row + m] = s.by;
   const uint32_t c = f8_codes(f2_make(x.x, x.y), f2_make(x.z, x.w), s);
   uint8_t* const o = q.data + m * q.row_bytes + n;

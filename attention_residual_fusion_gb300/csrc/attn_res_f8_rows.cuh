@@ -2,6 +2,8 @@
 // 128, its inverse, and the backward pass of the gated block.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_res_f8.cuh"
 #include "attn_res_tcgen05.cuh"
 
@@ -49,11 +51,12 @@ __device__ __forceinline__ void st_codes4(uint8_t* row, int64_t col, int64_t col
   }
 }
 
-// The scales of the strip's rows from each lane's maxima over its columns:
-// lane i makes that of row i, every lane gets all through shuffles.
+// The scales of the strip's rows from each lane's maxima over its columns: lane
+// i makes that of row i, all lanes get them through shared memory.
 struct StripScales {
   F8Scale mine;
-  __device__ __forceinline__ explicit StripScales(const uint32_t (&amax)[kF8Strip]) {
+  const F8Scale* all;
+  __device__ __forceinline__ StripScales(const uint32_t (&amax)[kF8Strip], F8Scale (&shared)[kF8Strip]) : all(shared) {
     const int lane = threadIdx.x & 31;
     uint32_t m = 0;
 #pragma unroll
@@ -62,13 +65,14 @@ struct StripScales {
       if (lane == i) m = r;
     }
     mine = f8_scale(m);
+    if (lane < kF8Strip) shared[lane] = mine;
+    __syncwarp();
   }
-  __device__ __forceinline__ F8Scale of(int i) const {
-    F8Scale s;
-    s.by = __shfl_sync(0xffffffffu, mine.by, i);
-    s.inverse = __shfl_sync(0xffffffffu, mine.inverse, i);
-    return s;
+  __device__ __forceinline__ bool held() const {
+    return __all_sync(0xffffffffu, f8_quotients_held(mine.by) || (threadIdx.x & 31) >= kF8Strip);
   }
+  // of rows i and i + 1 (i even): (by, inverse) twice
+  __device__ __forceinline__ float4 two(int i) const { return *reinterpret_cast<const float4*>(&all[i]); }
   // the lanes' scales into the matrix (rows row0 + lane of column block b)
   __device__ __forceinline__ void store(const F8View& q, int64_t row0, int64_t b) const {
     const int lane = threadIdx.x & 31;
@@ -86,7 +90,8 @@ struct StripScales {
 struct TileShared {
   uint4 codes[128][8];
   uint32_t amax[8][128];
-  F8Scale scale[128];
+  __align__(16) F8Scale scale[128];
+  __align__(16) F8Scale row_scale[8][kF8Strip];
 };
 
 __device__ __forceinline__ uint4& tile_piece(TileShared& t, int col, int piece) {
@@ -138,14 +143,31 @@ struct F8QuantizeParams {
   F8View q, t;  // t: the transposed matrix (the tile kernel)
 };
 
-// |x| of four bf16 as fp32 bits.
+// The largest of two bf16 magnitudes as fp32 bits, of a pair and of four values.
+__device__ __forceinline__ uint32_t pair_amax(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+__device__ __forceinline__ uint2 magnitudes(uint2 v) { return make_uint2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu); }
 __device__ __forceinline__ uint32_t bf16x4_amax(uint2 v) {
-  const uint32_t m = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
-  return max(m << 16, m & 0xffff0000u);
+  const uint2 m = magnitudes(v);
+  return pair_amax(__vmaxu2(m.x, m.y));
+}
+
+// A strip again, from memory, whose quotients want the division itself: rows with
+// scales outside 2^-96 .. 2^96 or without one.  (In the strip's own way its code
+// would lie between that of every four codes: 8192 x 7168 took 47.5 us.)
+__device__ __noinline__ void far_strip(const F8QuantizeParams& p, int64_t row0, int64_t b) {
+  const int lane = threadIdx.x & 31;
+  const int64_t col = b * kF8Block + 4 * lane;
+#pragma unroll 1
+  for (int64_t row = row0; row < row0 + kF8Strip && row < p.q.rows; ++row) {
+    const uint2 x = ld_bf16x4(p.x + row * p.x_row, col, p.q.cols);
+    const F8Scale s = f8_scale(__reduce_max_sync(0xffffffffu, bf16x4_amax(x)));
+    st_codes4(p.q.data + row * p.q.row_bytes, col, p.q.cols, f8_codes_far(bf2_widen(x.x), bf2_widen(x.y), s.by));
+  }
 }
 
 // Rows only: a warp a strip.
-__global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_rows_kernel(const F8QuantizeParams p) {
+__global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_rows_kernel(const __grid_constant__ F8QuantizeParams p) {
+  __shared__ __align__(16) F8Scale scale[kF8Threads / 32][kF8Strip];
   const int lane = threadIdx.x & 31;
   const int64_t blocks = f8_blocks(p.q.cols);
   const int64_t job = (int64_t)blockIdx.x * (kF8Threads / 32) + (threadIdx.x >> 5);
@@ -161,13 +183,19 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_rows_kernel(c
       x[i] = i < rows ? ld_bf16x4(p.x + (row0 + i) * p.x_row, col, p.q.cols) : make_uint2(0, 0);
 #pragma unroll
     for (int i = 0; i < kF8Strip; ++i) am[i] = bf16x4_amax(x[i]);
-    const StripScales s(am);
+    const StripScales s(am, scale[threadIdx.x >> 5]);
     s.store(p.q, row0, b);
+    if (s.held()) {
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) {
-      const F8Scale si = s.of(i);
-      if (i < rows)
-        st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), si));
+      for (int i = 0; i < kF8Strip; i += 2) {
+        const float4 si = s.two(i);
+        const uint32_t c0 = f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), si.x, si.y);
+        const uint32_t c1 = f8_codes(bf2_widen(x[i + 1].x), bf2_widen(x[i + 1].y), si.z, si.w);
+        if (i < rows) st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, c0);
+        if (i + 1 < rows) st_codes4(p.q.data + (row0 + i + 1) * p.q.row_bytes, col, p.q.cols, c1);
+      }
+    } else {
+      far_strip(p, row0, b);
     }
   }
   grid_dep_launch_dependents();
@@ -176,7 +204,7 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_rows_kernel(c
 // Tiles: block scales (SQUARE), or row scales with the transposed matrix too;
 // TRANSPOSED: the transposed matrix.
 template <bool SQUARE, bool TRANSPOSED>
-__global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_tile_kernel(const F8QuantizeParams p) {
+__global__ void __launch_bounds__(kF8Threads, 4) attn_res_f8_quantize_tile_kernel(const __grid_constant__ F8QuantizeParams p) {
   __shared__ TileShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blocks = f8_blocks(p.q.cols);
@@ -188,7 +216,6 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_tile_kernel(c
 #pragma unroll
   for (int i = 0; i < kF8Strip; ++i)
     x[i] = i < rows ? ld_bf16x4(p.x + (row0 + i) * p.x_row, col, p.q.cols) : make_uint2(0, 0);
-  uint32_t codes[4][4] = {};  // [column][quarter of the strip's rows]
   if constexpr (SQUARE) {
     uint32_t m = 0;
 #pragma unroll
@@ -203,48 +230,94 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_tile_kernel(c
       p.q.scales[rb * p.q.scales_row + cb] = s.by;
       if (TRANSPOSED) p.t.scales[cb * p.t.scales_row + rb] = s.by;
     }
+    auto encode = [&](auto far) {
+      uint32_t codes[4][4] = {};  // [column][quarter of the strip's rows]
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) {
-      const uint32_t c = f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), s);
-      if (i < rows) st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, c);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t c[4];  // of four rows, turned into those of four columns
 #pragma unroll
-      for (int j = 0; j < 4; ++j) codes[j][i / 4] |= (c >> (8 * j) & 0xffu) << (8 * (i % 4));
-    }
+        for (int i = 0; i < 4; ++i) {
+          const uint2 v = x[4 * k + i];
+          c[i] = decltype(far)::value ? f8_codes_far(bf2_widen(v.x), bf2_widen(v.y), s.by)
+                                      : f8_codes(bf2_widen(v.x), bf2_widen(v.y), s.by, s.inverse);
+          if (4 * k + i < rows) st_codes4(p.q.data + (row0 + 4 * k + i) * p.q.row_bytes, col, p.q.cols, c[i]);
+        }
+        if constexpr (TRANSPOSED) {
+          const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);
+          const uint32_t d = __byte_perm(c[0], c[1], 0x7362), e = __byte_perm(c[2], c[3], 0x7362);
+          codes[0][k] = __byte_perm(a, b, 0x5410);
+          codes[1][k] = __byte_perm(a, b, 0x7632);
+          codes[2][k] = __byte_perm(d, e, 0x5410);
+          codes[3][k] = __byte_perm(d, e, 0x7632);
+        }
+      }
+      if constexpr (TRANSPOSED)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
+    };
+    if (f8_quotients_held(s.by)) encode(std::false_type());
+    else encode(std::true_type());
   } else {
-    uint32_t am[kF8Strip], cm[4] = {};
+    uint32_t am[kF8Strip], cm2[2] = {};
 #pragma unroll
     for (int i = 0; i < kF8Strip; ++i) {
-      am[i] = bf16x4_amax(x[i]);
-      cm[0] = max(cm[0], x[i].x << 16 & 0x7fff0000u);
-      cm[1] = max(cm[1], x[i].x & 0x7fff0000u);
-      cm[2] = max(cm[2], x[i].y << 16 & 0x7fff0000u);
-      cm[3] = max(cm[3], x[i].y & 0x7fff0000u);
+      const uint2 m = magnitudes(x[i]);
+      am[i] = pair_amax(__vmaxu2(m.x, m.y));
+      cm2[0] = __vmaxu2(cm2[0], m.x);
+      cm2[1] = __vmaxu2(cm2[1], m.y);
     }
-    const StripScales s(am);
+    const uint32_t cm[4] = {cm2[0] << 16, cm2[0] & 0xffff0000u, cm2[1] << 16, cm2[1] & 0xffff0000u};
+    const StripScales s(am, sh.row_scale[warp]);
     s.store(p.q, row0, cb);
-#pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) {
-      const F8Scale si = s.of(i);
-      if (i < rows)
-        st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), si));
-    }
     tile_column_scales(sh, cm, p.t, col0, rb);
+    const float4* const scale = reinterpret_cast<const float4*>(&sh.scale[4 * lane]);  // (by, inverse) of two columns each
+    const float4 s01 = scale[0], s23 = scale[1];
+    const bool held = s.held();
+    if (held && __all_sync(0xffffffffu, f8_quotients_held(s01.x) && f8_quotients_held(s01.z) &&
+                                            f8_quotients_held(s23.x) && f8_quotients_held(s23.z))) {
+      const f32x2 by0 = f2_make(s01.x, s01.z), by1 = f2_make(s23.x, s23.z);
+      const f32x2 minus0 = f2_make(-s01.y, -s01.w), minus1 = f2_make(-s23.y, -s23.w);
+      uint32_t codes[4][4];  // [column][quarter of the strip's rows]
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const F8Scale sj = sh.scale[4 * lane + j];
-      auto value = [&](int i) {
-        const uint32_t w = j < 2 ? x[i].x : x[i].y;
-        return j % 2 ? bf_hi(w) : bf_lo(w);
-      };
+      for (int k = 0; k < 4; ++k) {
+        f32x2 c0[4], c1[4];  // columns' quotients, negated
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        codes[j][k] = f8_codes(f2_make(value(4 * k), value(4 * k + 1)), f2_make(value(4 * k + 2), value(4 * k + 3)), sj);
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * k + e;
+          const f32x2 lo = bf2_widen(x[i].x), hi = bf2_widen(x[i].y);
+          const float4 two = s.two(i & ~1);
+          const uint32_t c = f8_codes(lo, hi, e % 2 ? two.z : two.x, e % 2 ? two.w : two.y);
+          if (i < rows) st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, c);
+          c0[e] = f8_negated_quotient2(lo, by0, minus0);
+          c1[e] = f8_negated_quotient2(hi, by1, minus1);
+        }
+        codes[0][k] = e4m3x4(f2_lo(c0[0]), f2_lo(c0[1]), f2_lo(c0[2]), f2_lo(c0[3])) ^ 0x80808080u;
+        codes[1][k] = e4m3x4(f2_hi(c0[0]), f2_hi(c0[1]), f2_hi(c0[2]), f2_hi(c0[3])) ^ 0x80808080u;
+        codes[2][k] = e4m3x4(f2_lo(c1[0]), f2_lo(c1[1]), f2_lo(c1[2]), f2_lo(c1[3])) ^ 0x80808080u;
+        codes[3][k] = e4m3x4(f2_hi(c1[0]), f2_hi(c1[1]), f2_hi(c1[2]), f2_hi(c1[3])) ^ 0x80808080u;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
+    } else {
+      far_strip(p, row0, cb);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float by = j == 0 ? s01.x : j == 1 ? s01.z : j == 2 ? s23.x : s23.z;
+        auto value = [&](int i) {
+          const uint32_t w = j < 2 ? x[i].x : x[i].y;
+          return j % 2 ? bf_hi(w) : bf_lo(w);
+        };
+        uint32_t codes[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          codes[k] = f8_codes_far(f2_make(value(4 * k), value(4 * k + 1)), f2_make(value(4 * k + 2), value(4 * k + 3)), by);
+        tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+      }
     }
   }
   if constexpr (TRANSPOSED) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
     __syncthreads();
     tile_store_transposed(sh, p.t, col0, rb * kF8Block);
   }
@@ -306,7 +379,7 @@ __global__ void __launch_bounds__(kF8Threads) attn_res_f8_dequantize_kernel(cons
 // one, and about as many are needed: a value is made once and stays in
 // registers until both its scales are known (512 threads, 8 rows x 4 columns of
 // a 128 x 128 tile each, 96 values), and codes are made with the scale's
-// inverse.  That leaves room for one CTA an SM, so the CTAs are persistent and
+// inverse, which is off by less than the values are.  That leaves room for one CTA an SM, so the CTAs are persistent and
 // the next tile's inputs are brought in by TMA meanwhile.
 constexpr int kF8BackThreads = 512;
 constexpr int kF8BackRows = 8;  // of a warp
@@ -331,11 +404,11 @@ struct F8BackShared {
   F8BackStage stage[2];
   uint2 codes[3][128][16];  // [dg, du, h][column][8 rows], places mixed
   uint32_t amax[3][128];
-  float inverse[3][128];
+  float column_inverse[3][128];
+  float2 inverse[16][kF8BackRows];  // of a warp's rows, dg's and du's
   unsigned long long full[2];
 };
 
-// The codes of four values with a scale's inverse (NaN: none).
 __device__ __forceinline__ uint32_t codes_by(f32x2 a, f32x2 b) {
   return e4m3x4(f2_lo(a), f2_hi(a), f2_lo(b), f2_hi(b));
 }
@@ -394,7 +467,7 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(uc) : "r"(smem_addr(&in.u[r][4 * lane])) : "memory");
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sg) : "r"(smem_addr(&in.g_scales[r])) : "memory");
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(su) : "r"(smem_addr(&in.u_scales[r])) : "memory");
-      uint32_t a = 0, b = 0;
+      float a = 0.f, b = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const f32x2 g = f2_mul(e4m3_pair(gc >> (16 * j)), f2_make(sg, sg));
@@ -408,14 +481,14 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
         // (rows and columns behind the last were read as zeros: they count for
         // nothing where the row's scales are numbers, and where one is none the
         // row's values are none either)
-        a = max(a, max(magnitude(f2_lo(dg[i][j])), magnitude(f2_hi(dg[i][j]))));
-        b = max(b, max(magnitude(f2_lo(du[i][j])), magnitude(f2_hi(du[i][j]))));
+        a = amax3(a, dg[i][j]);
+        b = amax3(b, du[i][j]);
       }
-      a = __reduce_max_sync(0xffffffffu, a);
-      b = __reduce_max_sync(0xffffffffu, b);
+      a = warp_amax(a);
+      b = warp_amax(b);
       if (lane == i) {
-        am_g = a;
-        am_u = b;
+        am_g = __float_as_uint(a);
+        am_u = __float_as_uint(b);
       }
     }
     if constexpr (TRANSPOSED) {
@@ -423,15 +496,16 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
       for (int which = 0; which < 3; ++which)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t lo = 0, hi = 0;
+          float lo = 0.f, hi = 0.f;
 #pragma unroll
-          for (int i = 0; i < kF8BackRows; ++i) {
+          for (int i = 0; i < kF8BackRows; i += 2) {
             const f32x2 v = which == 0 ? dg[i][j] : which == 1 ? du[i][j] : h[i][j];
-            lo = max(lo, magnitude(f2_lo(v)));
-            hi = max(hi, magnitude(f2_hi(v)));
+            const f32x2 w = which == 0 ? dg[i + 1][j] : which == 1 ? du[i + 1][j] : h[i + 1][j];
+            lo = amax3(lo, f2_lo(v), f2_lo(w));
+            hi = amax3(hi, f2_hi(v), f2_hi(w));
           }
-          atomicMax(&sh.amax[which][4 * lane + 2 * j], lo);
-          atomicMax(&sh.amax[which][4 * lane + 2 * j + 1], hi);
+          atomicMax(&sh.amax[which][4 * lane + 2 * j], __float_as_uint(lo));
+          atomicMax(&sh.amax[which][4 * lane + 2 * j + 1], __float_as_uint(hi));
         }
     }
     __syncthreads();  // the stage has been read, the columns' maxima are there
@@ -443,7 +517,7 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
     if (TRANSPOSED && threadIdx.x < 3 * 128) {
       const int which = threadIdx.x / 128, c = threadIdx.x % 128;
       const F8Scale sc = f8_scale(sh.amax[which][c]);
-      sh.inverse[which][c] = sc.inverse;
+      sh.column_inverse[which][c] = sc.inverse;
       sh.amax[which][c] = 0;
       const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
       if (col0 + c < cols && !failed) t.scales[rb * t.scales_row + col0 + c] = sc.by;
@@ -452,14 +526,19 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
       p.dg.scales[cb * p.dg.scales_row + row0 + lane] = sg.by;
       p.du.scales[cb * p.du.scales_row + row0 + lane] = su.by;
     }
+    if (lane < kF8BackRows) sh.inverse[warp][lane] = make_float2(sg.inverse, su.inverse);
+    __syncwarp();
+    const bool no_number = __any_sync(0xffffffffu, sg.by != sg.by || su.by != su.by);
 #pragma unroll
     for (int i = 0; i < kF8BackRows; ++i) {
-      const float ig = __shfl_sync(0xffffffffu, sg.inverse, i), iu = __shfl_sync(0xffffffffu, su.inverse, i);
-      const f32x2 by_g = f2_make(ig, ig), by_u = f2_make(iu, iu);
+      const float2 inv = sh.inverse[warp][i];
+      const f32x2 by_g = f2_make(inv.x, inv.x), by_u = f2_make(inv.y, inv.y);
       uint32_t a = codes_by(f2_mul(dg[i][0], by_g), f2_mul(dg[i][1], by_g));
       uint32_t b = codes_by(f2_mul(du[i][0], by_u), f2_mul(du[i][1], by_u));
-      if (ig != ig) a = 0;
-      if (iu != iu) b = 0;
+      if (no_number) {
+        if (inv.x != inv.x) a = 0;
+        if (inv.y != inv.y) b = 0;
+      }
       if (row0 + i < rows && !failed) {
         st_codes4(p.dg.data + (row0 + i) * p.dg.row_bytes, col, cols, a);
         st_codes4(p.du.data + (row0 + i) * p.du.row_bytes, col, cols, b);
@@ -469,11 +548,10 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
       __syncthreads();  // the inverses are there; the codes of the tile before have left
 #pragma unroll
       for (int which = 0; which < 3; ++which) {
-        const float4 inv = *reinterpret_cast<const float4*>(&sh.inverse[which][4 * lane]);
+        const float4 inv = *reinterpret_cast<const float4*>(&sh.column_inverse[which][4 * lane]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float i0 = j ? inv.z : inv.x, i1 = j ? inv.w : inv.y;
-          const f32x2 by = f2_make(i0, i1);
+          const f32x2 by = j ? f2_make(inv.z, inv.w) : f2_make(inv.x, inv.y);
           f32x2 v[kF8BackRows];
 #pragma unroll
           for (int i = 0; i < kF8BackRows; ++i) v[i] = f2_mul(which == 0 ? dg[i][j] : which == 1 ? du[i][j] : h[i][j], by);
@@ -482,8 +560,11 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
           lo.y = e4m3x4(f2_lo(v[4]), f2_lo(v[5]), f2_lo(v[6]), f2_lo(v[7]));
           hi.x = e4m3x4(f2_hi(v[0]), f2_hi(v[1]), f2_hi(v[2]), f2_hi(v[3]));
           hi.y = e4m3x4(f2_hi(v[4]), f2_hi(v[5]), f2_hi(v[6]), f2_hi(v[7]));
-          if (i0 != i0) lo = make_uint2(0, 0);
-          if (i1 != i1) hi = make_uint2(0, 0);
+          const float sum = f2_lo(by) + f2_hi(by);
+          if (sum != sum) {  // a column without a scale
+            if (f2_lo(by) != f2_lo(by)) lo = make_uint2(0, 0);
+            if (f2_hi(by) != f2_hi(by)) hi = make_uint2(0, 0);
+          }
           // column c's piece of warp w at w ^ (c / 4 % 16): writes and reads
           // without bank conflicts
           sh.codes[which][4 * lane + 2 * j][warp ^ (lane & 15)] = lo;

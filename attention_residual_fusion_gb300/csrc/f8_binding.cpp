@@ -62,11 +62,11 @@ F8Tensor make(const at::Tensor& data, const at::Tensor& scales, int block) {
   return t;
 }
 
-// Rows of codes a multiple of 16 bytes apart, rows of scales of 16 bytes too.
+// Rows of codes a multiple of 16 bytes apart, rows of scales of 16 bytes too (the
+// last row without its padding, which nothing touches).
 at::Tensor padded(int64_t rows, int64_t cols, int64_t to, at::ScalarType type, at::Device device) {
-  const int64_t row = (cols + to - 1) / to * to;
-  at::Tensor t = new_tensor({rows, row}, type, device);
-  return row == cols ? t : t.narrow(1, 0, cols);
+  const int64_t size[2] = {rows, cols}, stride[2] = {(cols + to - 1) / to * to, 1};
+  return at::detail::empty_strided_cuda(size, stride, type, device);
 }
 F8Tensor allocate(int64_t rows, int64_t cols, int block, at::Device device) {
   const auto s = scales_shape(rows, cols, block);
