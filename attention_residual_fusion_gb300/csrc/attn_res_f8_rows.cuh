@@ -19,36 +19,54 @@ constexpr int kF8Strip = 16;  // rows of a warp's strip, 128 columns wide
 // column stays in its lane, and the 16 codes of a column are one 16-byte piece
 // of the transposed matrix.
 
-// Four bf16 of a row from column `col` on, zeros behind the last.
-__device__ __forceinline__ uint2 ld_bf16x4(const uint16_t* row, int64_t col, int64_t cols) {
-  if (col + 4 <= cols) {
+// Most strips and tiles are whole: their code (WHOLE = 2) asks for no row or
+// column (8192 x 7168 with both outputs 68 us when each access did), that of few
+// rows of whole columns (1) for rows.  Addresses are a lane's first one and, for
+// all lanes alike, rows times a stride.
+//
+// Four bf16 from `at` on, `left` columns before the row's last; zeros behind it,
+// and where `in` is false.
+template <int WHOLE>
+__device__ __forceinline__ uint2 ld_bf16x4(const uint16_t* at, int64_t left, bool in = true) {
+  if (WHOLE == 2 || (in && (WHOLE == 1 || left >= 4))) {
     uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(row + col));
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(at));
     return v;
   }
+  if (WHOLE == 1) return make_uint2(0, 0);
   uint32_t e[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (col + k < cols) e[k] = row[col + k];
+    if (in && k < left) e[k] = at[k];
   return make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
 }
 // Four codes.
-__device__ __forceinline__ uint32_t ld_codes4(const uint8_t* row, int64_t col, int64_t cols) {
-  if (col + 4 <= cols) return *reinterpret_cast<const uint32_t*>(row + col);
+template <int WHOLE>
+__device__ __forceinline__ uint32_t ld_codes4(const uint8_t* at, int64_t left, bool in = true) {
+  if (WHOLE == 2 || (in && (WHOLE == 1 || left >= 4))) return *reinterpret_cast<const uint32_t*>(at);
+  if (WHOLE == 1) return 0u;
   uint32_t v = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (col + k < cols) v |= (uint32_t)row[col + k] << (8 * k);
+    if (in && k < left) v |= (uint32_t)at[k] << (8 * k);
   return v;
 }
-__device__ __forceinline__ void st_codes4(uint8_t* row, int64_t col, int64_t cols, uint32_t v) {
-  if (col + 4 <= cols) {
-    *reinterpret_cast<uint32_t*>(row + col) = v;
-  } else {
+template <int WHOLE>
+__device__ __forceinline__ void st_codes4(uint8_t* at, int64_t left, uint32_t v, bool in = true) {
+  if (WHOLE == 2 || (in && (WHOLE == 1 || left >= 4))) {
+    *reinterpret_cast<uint32_t*>(at) = v;
+  } else if (WHOLE == 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (col + k < cols) row[col + k] = (uint8_t)(v >> (8 * k));
+      if (in && k < left) at[k] = (uint8_t)(v >> (8 * k));
   }
+}
+// f(integral constant).
+template <class Fn>
+__device__ __forceinline__ void with_whole(bool rows, bool cols, Fn f) {
+  if (rows && cols) f(std::integral_constant<int, 2>());
+  else if (cols) f(std::integral_constant<int, 1>());
+  else f(std::integral_constant<int, 0>());
 }
 
 // The scales of the strip's rows from each lane's maxima over its columns: lane
@@ -118,19 +136,23 @@ __device__ __forceinline__ void tile_column_scales(TileShared& t, const uint32_t
 }
 
 // The transposed codes from shared memory to qt: rows col0 .., bytes row0 ..
+template <bool WHOLE>
 __device__ __forceinline__ void tile_store_transposed(TileShared& t, const F8View& qt, int64_t col0, int64_t row0) {
-  for (int i = threadIdx.x; i < 128 * 8; i += kF8Threads) {
-    const int c = i / 8, piece = i % 8;
-    const int64_t at = row0 + 16 * piece;
-    if (col0 + c >= qt.rows || at >= qt.cols) continue;
-    const uint4 v = tile_piece(t, c, piece);
-    uint8_t* const o = qt.data + (col0 + c) * qt.row_bytes + at;
-    if (at + 16 <= qt.cols) {
-      *reinterpret_cast<uint4*>(o) = v;
-    } else {
+  constexpr int STEP = kF8Threads / 8;  // columns
+  const int c0 = threadIdx.x / 8, piece = threadIdx.x % 8;
+  const int64_t at = row0 + 16 * piece;
+  uint8_t* const first = qt.data + (col0 + c0) * qt.row_bytes + at;
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (at + k < qt.cols) o[k] = (uint8_t)(vword(v, k / 4) >> (8 * (k % 4)));
+  for (int k = 0; k < 128 / STEP; ++k) {
+    const int c = c0 + STEP * k;
+    uint8_t* const o = first + k * STEP * qt.row_bytes;
+    if (WHOLE || (col0 + c < qt.rows && at + 16 <= qt.cols)) {
+      *reinterpret_cast<uint4*>(o) = tile_piece(t, c, piece);
+    } else if (col0 + c < qt.rows) {
+      const uint4 v = tile_piece(t, c, piece);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (at + e < qt.cols) o[e] = (uint8_t)(vword(v, e / 4) >> (8 * (e % 4)));
     }
   }
 }
@@ -153,52 +175,64 @@ __device__ __forceinline__ uint32_t bf16x4_amax(uint2 v) {
 
 // A strip again, from memory, whose quotients want the division itself: rows with
 // scales outside 2^-96 .. 2^96 or without one.  (In the strip's own way its code
-// would lie between that of every four codes: 8192 x 7168 took 47.5 us.)
+// would lie between that of every four codes: 8192 x 7168 47.5 us instead of 43.)
 __device__ __noinline__ void far_strip(const F8QuantizeParams& p, int64_t row0, int64_t b) {
   const int lane = threadIdx.x & 31;
-  const int64_t col = b * kF8Block + 4 * lane;
+  const int64_t col = b * kF8Block + 4 * lane, left = p.q.cols - col;
 #pragma unroll 1
   for (int64_t row = row0; row < row0 + kF8Strip && row < p.q.rows; ++row) {
-    const uint2 x = ld_bf16x4(p.x + row * p.x_row, col, p.q.cols);
+    const uint2 x = ld_bf16x4<0>(p.x + row * p.x_row + col, left);
     const F8Scale s = f8_scale(__reduce_max_sync(0xffffffffu, bf16x4_amax(x)));
-    st_codes4(p.q.data + row * p.q.row_bytes, col, p.q.cols, f8_codes_far(bf2_widen(x.x), bf2_widen(x.y), s.by));
+    st_codes4<0>(p.q.data + row * p.q.row_bytes + col, left, f8_codes_far(bf2_widen(x.x), bf2_widen(x.y), s.by));
   }
 }
 
 // Rows only: a warp a strip.
 __global__ void __launch_bounds__(kF8Threads) attn_res_f8_quantize_rows_kernel(const __grid_constant__ F8QuantizeParams p) {
   __shared__ __align__(16) F8Scale scale[kF8Threads / 32][kF8Strip];
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blocks = f8_blocks(p.q.cols);
-  const int64_t job = (int64_t)blockIdx.x * (kF8Threads / 32) + (threadIdx.x >> 5);
+  const int64_t job = (int64_t)blockIdx.x * (kF8Threads / 32) + warp;
   const int64_t row0 = job / blocks * kF8Strip, b = job % blocks;
   grid_dep_wait();
   if (row0 < p.q.rows) {
-    const int64_t col = b * kF8Block + 4 * lane;
+    const int64_t col = b * kF8Block + 4 * lane, left = p.q.cols - col;
     const int rows = (int)(p.q.rows - row0 < kF8Strip ? p.q.rows - row0 : kF8Strip);
-    uint2 x[kF8Strip];
-    uint32_t am[kF8Strip];
+    const uint16_t* const from = p.x + row0 * p.x_row + col;
+    uint8_t* const to = p.q.data + row0 * p.q.row_bytes + col;
+    with_whole(rows == kF8Strip, (b + 1) * kF8Block <= p.q.cols, [&](auto whole) {
+      constexpr int W = decltype(whole)::value;
+      uint2 x[kF8Strip];
+      uint32_t am[kF8Strip];
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i)
-      x[i] = i < rows ? ld_bf16x4(p.x + (row0 + i) * p.x_row, col, p.q.cols) : make_uint2(0, 0);
+      for (int i = 0; i < kF8Strip; ++i) x[i] = ld_bf16x4<W>(from + i * p.x_row, left, i < rows);
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) am[i] = bf16x4_amax(x[i]);
-    const StripScales s(am, scale[threadIdx.x >> 5]);
-    s.store(p.q, row0, b);
-    if (s.held()) {
+      for (int i = 0; i < kF8Strip; ++i) am[i] = bf16x4_amax(x[i]);
+      const StripScales s(am, scale[warp]);
+      s.store(p.q, row0, b);
+      if (s.held()) {
 #pragma unroll
-      for (int i = 0; i < kF8Strip; i += 2) {
-        const float4 si = s.two(i);
-        const uint32_t c0 = f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), si.x, si.y);
-        const uint32_t c1 = f8_codes(bf2_widen(x[i + 1].x), bf2_widen(x[i + 1].y), si.z, si.w);
-        if (i < rows) st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, c0);
-        if (i + 1 < rows) st_codes4(p.q.data + (row0 + i + 1) * p.q.row_bytes, col, p.q.cols, c1);
+        for (int i = 0; i < kF8Strip; i += 2) {
+          const float4 si = s.two(i);
+          st_codes4<W>(to + i * p.q.row_bytes, left, f8_codes(bf2_widen(x[i].x), bf2_widen(x[i].y), si.x, si.y), i < rows);
+          st_codes4<W>(to + (i + 1) * p.q.row_bytes, left,
+                       f8_codes(bf2_widen(x[i + 1].x), bf2_widen(x[i + 1].y), si.z, si.w), i + 1 < rows);
+        }
+      } else {
+        far_strip(p, row0, b);
       }
-    } else {
-      far_strip(p, row0, b);
-    }
+    });
   }
   grid_dep_launch_dependents();
+}
+
+// Columns' codes of four rows (their quotients in pairs of columns, negated), the
+// first row lowest.
+__device__ __forceinline__ uint32_t codes_lo(const f32x2 (&v)[4]) {
+  return e4m3x4(f2_lo(v[0]), f2_lo(v[1]), f2_lo(v[2]), f2_lo(v[3])) ^ 0x80808080u;
+}
+__device__ __forceinline__ uint32_t codes_hi(const f32x2 (&v)[4]) {
+  return e4m3x4(f2_hi(v[0]), f2_hi(v[1]), f2_hi(v[2]), f2_hi(v[3])) ^ 0x80808080u;
 }
 
 // Tiles: block scales (SQUARE), or row scales with the transposed matrix too;
@@ -209,118 +243,125 @@ __global__ void __launch_bounds__(kF8Threads, 4) attn_res_f8_quantize_tile_kerne
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blocks = f8_blocks(p.q.cols);
   const int64_t rb = blockIdx.x / blocks, cb = blockIdx.x % blocks;
-  const int64_t row0 = rb * kF8Block + warp * kF8Strip, col0 = cb * kF8Block, col = col0 + 4 * lane;
+  const int64_t row0 = rb * kF8Block + warp * kF8Strip, col0 = cb * kF8Block, col = col0 + 4 * lane, left = p.q.cols - col;
   const int rows = (int)(p.q.rows - row0 < kF8Strip ? p.q.rows - row0 : kF8Strip);  // (may be negative)
+  const uint16_t* const from = p.x + row0 * p.x_row + col;
+  uint8_t* const to = p.q.data + row0 * p.q.row_bytes + col;
   grid_dep_wait();
-  uint2 x[kF8Strip];
+  with_whole((rb + 1) * kF8Block <= p.q.rows, col0 + kF8Block <= p.q.cols, [&](auto whole) {
+    constexpr int W = decltype(whole)::value;
+    uint2 x[kF8Strip];
 #pragma unroll
-  for (int i = 0; i < kF8Strip; ++i)
-    x[i] = i < rows ? ld_bf16x4(p.x + (row0 + i) * p.x_row, col, p.q.cols) : make_uint2(0, 0);
-  if constexpr (SQUARE) {
-    uint32_t m = 0;
+    for (int i = 0; i < kF8Strip; ++i) x[i] = ld_bf16x4<W>(from + i * p.x_row, left, i < rows);
+    if constexpr (SQUARE) {
+      uint2 m2 = make_uint2(0, 0);
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) m = max(m, bf16x4_amax(x[i]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) sh.amax[0][warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, sh.amax[0][w]);
-    const F8Scale s = f8_scale(m);
-    if (threadIdx.x == 0) {
-      p.q.scales[rb * p.q.scales_row + cb] = s.by;
-      if (TRANSPOSED) p.t.scales[cb * p.t.scales_row + rb] = s.by;
-    }
-    auto encode = [&](auto far) {
-      uint32_t codes[4][4] = {};  // [column][quarter of the strip's rows]
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t c[4];  // of four rows, turned into those of four columns
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 v = x[4 * k + i];
-          c[i] = decltype(far)::value ? f8_codes_far(bf2_widen(v.x), bf2_widen(v.y), s.by)
-                                      : f8_codes(bf2_widen(v.x), bf2_widen(v.y), s.by, s.inverse);
-          if (4 * k + i < rows) st_codes4(p.q.data + (row0 + 4 * k + i) * p.q.row_bytes, col, p.q.cols, c[i]);
-        }
-        if constexpr (TRANSPOSED) {
-          const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);
-          const uint32_t d = __byte_perm(c[0], c[1], 0x7362), e = __byte_perm(c[2], c[3], 0x7362);
-          codes[0][k] = __byte_perm(a, b, 0x5410);
-          codes[1][k] = __byte_perm(a, b, 0x7632);
-          codes[2][k] = __byte_perm(d, e, 0x5410);
-          codes[3][k] = __byte_perm(d, e, 0x7632);
-        }
+      for (int i = 0; i < kF8Strip; ++i) {
+        const uint2 m = magnitudes(x[i]);
+        m2 = make_uint2(__vmaxu2(m2.x, m.x), __vmaxu2(m2.y, m.y));
       }
-      if constexpr (TRANSPOSED)
+      uint32_t m = __reduce_max_sync(0xffffffffu, pair_amax(__vmaxu2(m2.x, m2.y)));
+      if (lane == 0) sh.amax[0][warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = max(m, sh.amax[0][w]);
+      const F8Scale s = f8_scale(m);
+      if (threadIdx.x == 0) {
+        p.q.scales[rb * p.q.scales_row + cb] = s.by;
+        if (TRANSPOSED) p.t.scales[cb * p.t.scales_row + rb] = s.by;
+      }
+      auto encode = [&](auto far) {
+        uint32_t codes[4][4] = {};  // [column][quarter of the strip's rows]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t c[4];  // of four rows, turned into those of four columns
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 v = x[4 * k + i];
+            c[i] = decltype(far)::value ? f8_codes_far(bf2_widen(v.x), bf2_widen(v.y), s.by)
+                                        : f8_codes(bf2_widen(v.x), bf2_widen(v.y), s.by, s.inverse);
+            st_codes4<W>(to + (4 * k + i) * p.q.row_bytes, left, c[i], 4 * k + i < rows);
+          }
+          if constexpr (TRANSPOSED) {
+            const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);
+            const uint32_t d = __byte_perm(c[0], c[1], 0x7362), e = __byte_perm(c[2], c[3], 0x7362);
+            codes[0][k] = __byte_perm(a, b, 0x5410);
+            codes[1][k] = __byte_perm(a, b, 0x7632);
+            codes[2][k] = __byte_perm(d, e, 0x5410);
+            codes[3][k] = __byte_perm(d, e, 0x7632);
+          }
+        }
+        if constexpr (TRANSPOSED)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
+      };
+      if (f8_quotients_held(s.by)) encode(std::false_type());
+      else encode(std::true_type());
+    } else {
+      uint32_t am[kF8Strip], cm2[2] = {};
+#pragma unroll
+      for (int i = 0; i < kF8Strip; ++i) {
+        const uint2 m = magnitudes(x[i]);
+        am[i] = pair_amax(__vmaxu2(m.x, m.y));
+        cm2[0] = __vmaxu2(cm2[0], m.x);
+        cm2[1] = __vmaxu2(cm2[1], m.y);
+      }
+      const uint32_t cm[4] = {cm2[0] << 16, cm2[0] & 0xffff0000u, cm2[1] << 16, cm2[1] & 0xffff0000u};
+      const StripScales s(am, sh.row_scale[warp]);
+      s.store(p.q, row0, cb);
+      tile_column_scales(sh, cm, p.t, col0, rb);
+      const float4* const scale = reinterpret_cast<const float4*>(&sh.scale[4 * lane]);  // (by, inverse) of two columns each
+      const float4 s01 = scale[0], s23 = scale[1];
+      const bool held = s.held();
+      if (held && __all_sync(0xffffffffu, f8_quotients_held(s01.x) && f8_quotients_held(s01.z) &&
+                                              f8_quotients_held(s23.x) && f8_quotients_held(s23.z))) {
+        const f32x2 by0 = f2_make(s01.x, s01.z), by1 = f2_make(s23.x, s23.z);
+        const f32x2 minus0 = f2_make(-s01.y, -s01.w), minus1 = f2_make(-s23.y, -s23.w);
+        uint32_t codes[4][4];  // [column][quarter of the strip's rows]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f32x2 c0[4], c1[4];  // columns' quotients, negated
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * k + e;
+            const f32x2 lo = bf2_widen(x[i].x), hi = bf2_widen(x[i].y);
+            const float4 two = s.two(i & ~1);
+            st_codes4<W>(to + i * p.q.row_bytes, left,
+                         f8_codes(lo, hi, e % 2 ? two.z : two.x, e % 2 ? two.w : two.y), i < rows);
+            c0[e] = f8_negated_quotient2(lo, by0, minus0);
+            c1[e] = f8_negated_quotient2(hi, by1, minus1);
+          }
+          codes[0][k] = codes_lo(c0);
+          codes[1][k] = codes_hi(c0);
+          codes[2][k] = codes_lo(c1);
+          codes[3][k] = codes_hi(c1);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
-    };
-    if (f8_quotients_held(s.by)) encode(std::false_type());
-    else encode(std::true_type());
-  } else {
-    uint32_t am[kF8Strip], cm2[2] = {};
+      } else {
+        far_strip(p, row0, cb);
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) {
-      const uint2 m = magnitudes(x[i]);
-      am[i] = pair_amax(__vmaxu2(m.x, m.y));
-      cm2[0] = __vmaxu2(cm2[0], m.x);
-      cm2[1] = __vmaxu2(cm2[1], m.y);
-    }
-    const uint32_t cm[4] = {cm2[0] << 16, cm2[0] & 0xffff0000u, cm2[1] << 16, cm2[1] & 0xffff0000u};
-    const StripScales s(am, sh.row_scale[warp]);
-    s.store(p.q, row0, cb);
-    tile_column_scales(sh, cm, p.t, col0, rb);
-    const float4* const scale = reinterpret_cast<const float4*>(&sh.scale[4 * lane]);  // (by, inverse) of two columns each
-    const float4 s01 = scale[0], s23 = scale[1];
-    const bool held = s.held();
-    if (held && __all_sync(0xffffffffu, f8_quotients_held(s01.x) && f8_quotients_held(s01.z) &&
-                                            f8_quotients_held(s23.x) && f8_quotients_held(s23.z))) {
-      const f32x2 by0 = f2_make(s01.x, s01.z), by1 = f2_make(s23.x, s23.z);
-      const f32x2 minus0 = f2_make(-s01.y, -s01.w), minus1 = f2_make(-s23.y, -s23.w);
-      uint32_t codes[4][4];  // [column][quarter of the strip's rows]
+        for (int j = 0; j < 4; ++j) {
+          const float by = j == 0 ? s01.x : j == 1 ? s01.z : j == 2 ? s23.x : s23.z;
+          auto value = [&](int i) {
+            const uint32_t w = j < 2 ? x[i].x : x[i].y;
+            return j % 2 ? bf_hi(w) : bf_lo(w);
+          };
+          uint32_t codes[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f32x2 c0[4], c1[4];  // columns' quotients, negated
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 4 * k + e;
-          const f32x2 lo = bf2_widen(x[i].x), hi = bf2_widen(x[i].y);
-          const float4 two = s.two(i & ~1);
-          const uint32_t c = f8_codes(lo, hi, e % 2 ? two.z : two.x, e % 2 ? two.w : two.y);
-          if (i < rows) st_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols, c);
-          c0[e] = f8_negated_quotient2(lo, by0, minus0);
-          c1[e] = f8_negated_quotient2(hi, by1, minus1);
+          for (int k = 0; k < 4; ++k)
+            codes[k] = f8_codes_far(f2_make(value(4 * k), value(4 * k + 1)), f2_make(value(4 * k + 2), value(4 * k + 3)), by);
+          tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
         }
-        codes[0][k] = e4m3x4(f2_lo(c0[0]), f2_lo(c0[1]), f2_lo(c0[2]), f2_lo(c0[3])) ^ 0x80808080u;
-        codes[1][k] = e4m3x4(f2_hi(c0[0]), f2_hi(c0[1]), f2_hi(c0[2]), f2_hi(c0[3])) ^ 0x80808080u;
-        codes[2][k] = e4m3x4(f2_lo(c1[0]), f2_lo(c1[1]), f2_lo(c1[2]), f2_lo(c1[3])) ^ 0x80808080u;
-        codes[3][k] = e4m3x4(f2_hi(c1[0]), f2_hi(c1[1]), f2_hi(c1[2]), f2_hi(c1[3])) ^ 0x80808080u;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[j][0], codes[j][1], codes[j][2], codes[j][3]);
-    } else {
-      far_strip(p, row0, cb);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float by = j == 0 ? s01.x : j == 1 ? s01.z : j == 2 ? s23.x : s23.z;
-        auto value = [&](int i) {
-          const uint32_t w = j < 2 ? x[i].x : x[i].y;
-          return j % 2 ? bf_hi(w) : bf_lo(w);
-        };
-        uint32_t codes[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          codes[k] = f8_codes_far(f2_make(value(4 * k), value(4 * k + 1)), f2_make(value(4 * k + 2), value(4 * k + 3)), by);
-        tile_piece(sh, 4 * lane + j, warp) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
       }
     }
-  }
-  if constexpr (TRANSPOSED) {
-    __syncthreads();
-    tile_store_transposed(sh, p.t, col0, rb * kF8Block);
-  }
+    if constexpr (TRANSPOSED) {
+      __syncthreads();
+      tile_store_transposed<W == 2>(sh, p.t, col0, rb * kF8Block);
+    }
+  });
   grid_dep_launch_dependents();
 }
 
@@ -333,38 +374,41 @@ struct F8DequantizeParams {
 };
 
 template <bool SQUARE>
-__global__ void __launch_bounds__(kF8Threads) attn_res_f8_dequantize_kernel(const F8DequantizeParams p) {
+__global__ void __launch_bounds__(kF8Threads) attn_res_f8_dequantize_kernel(const __grid_constant__ F8DequantizeParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t blocks = f8_blocks(p.q.cols);
   const int64_t job = (int64_t)blockIdx.x * (kF8Threads / 32) + (threadIdx.x >> 5);
   const int64_t row0 = job / blocks * kF8Strip, b = job % blocks;
   grid_dep_wait();
   if (row0 < p.q.rows) {
-    const int64_t col = b * kF8Block + 4 * lane;
+    const int64_t col = b * kF8Block + 4 * lane, left = p.q.cols - col;
     const int rows = (int)(p.q.rows - row0 < kF8Strip ? p.q.rows - row0 : kF8Strip);
-    uint32_t c[kF8Strip];
+    const uint8_t* const from = p.q.data + row0 * p.q.row_bytes + col;
+    uint16_t* const to = p.x + row0 * p.x_row + col;
+    with_whole(rows == kF8Strip, (b + 1) * kF8Block <= p.q.cols, [&](auto whole) {
+      constexpr int W = decltype(whole)::value;
+      uint32_t c[kF8Strip];
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i)
-      c[i] = i < rows ? ld_codes4(p.q.data + (row0 + i) * p.q.row_bytes, col, p.q.cols) : 0u;
-    // (a strip lies in one block of rows)
-    float s = 0.f;
-    if (SQUARE) s = p.q.scales[row0 / kF8Block * p.q.scales_row + b];
-    else if (lane < rows) s = p.q.scales[b * p.q.scales_row + row0 + lane];
+      for (int i = 0; i < kF8Strip; ++i) c[i] = ld_codes4<W>(from + i * p.q.row_bytes, left, i < rows);
+      // (a strip lies in one block of rows)
+      float s = 0.f;
+      if (SQUARE) s = p.q.scales[row0 / kF8Block * p.q.scales_row + b];
+      else if (lane < rows) s = p.q.scales[b * p.q.scales_row + row0 + lane];
 #pragma unroll
-    for (int i = 0; i < kF8Strip; ++i) {
-      const float by = SQUARE ? s : __shfl_sync(0xffffffffu, s, i);
-      const f32x2 lo = f2_mul(e4m3_pair(c[i]), f2_make(by, by)), hi = f2_mul(e4m3_pair(c[i] >> 16), f2_make(by, by));
-      const uint32_t a = pack_bf16x2(f2_lo(lo), f2_hi(lo)), d = pack_bf16x2(f2_lo(hi), f2_hi(hi));
-      if (i >= rows) continue;
-      uint16_t* const o = p.x + (row0 + i) * p.x_row + col;
-      if (col + 4 <= p.q.cols) {
-        *reinterpret_cast<uint2*>(o) = make_uint2(a, d);
-      } else {
-        if (col < p.q.cols) o[0] = (uint16_t)a;
-        if (col + 1 < p.q.cols) o[1] = (uint16_t)(a >> 16);
-        if (col + 2 < p.q.cols) o[2] = (uint16_t)d;
+      for (int i = 0; i < kF8Strip; ++i) {
+        const float by = SQUARE ? s : __shfl_sync(0xffffffffu, s, i);
+        const f32x2 lo = f2_mul(e4m3_pair(c[i]), f2_make(by, by)), hi = f2_mul(e4m3_pair(c[i] >> 16), f2_make(by, by));
+        const uint32_t a = pack_bf16x2(f2_lo(lo), f2_hi(lo)), d = pack_bf16x2(f2_lo(hi), f2_hi(hi));
+        uint16_t* const o = to + i * p.x_row;
+        if (W == 2 || (i < rows && (W == 1 || left >= 4))) {
+          *reinterpret_cast<uint2*>(o) = make_uint2(a, d);
+        } else if (W == 0 && i < rows) {
+          if (left > 0) o[0] = (uint16_t)a;
+          if (left > 1) o[1] = (uint16_t)(a >> 16);
+          if (left > 2) o[2] = (uint16_t)d;
+        }
       }
-    }
+    });
   }
   grid_dep_launch_dependents();
 }
@@ -526,6 +570,9 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
       p.dg.scales[cb * p.dg.scales_row + row0 + lane] = sg.by;
       p.du.scales[cb * p.du.scales_row + row0 + lane] = su.by;
     }
+    uint8_t* const to_g = p.dg.data + row0 * p.dg.row_bytes + col;
+    uint8_t* const to_u = p.du.data + row0 * p.du.row_bytes + col;
+    const bool whole = (rb + 1) * 128 <= rows && col0 + 128 <= cols && !failed;
     if (lane < kF8BackRows) sh.inverse[warp][lane] = make_float2(sg.inverse, su.inverse);
     __syncwarp();
     const bool no_number = __any_sync(0xffffffffu, sg.by != sg.by || su.by != su.by);
@@ -539,9 +586,12 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
         if (inv.x != inv.x) a = 0;
         if (inv.y != inv.y) b = 0;
       }
-      if (row0 + i < rows && !failed) {
-        st_codes4(p.dg.data + (row0 + i) * p.dg.row_bytes, col, cols, a);
-        st_codes4(p.du.data + (row0 + i) * p.du.row_bytes, col, cols, b);
+      if (whole) {
+        *reinterpret_cast<uint32_t*>(to_g + i * p.dg.row_bytes) = a;
+        *reinterpret_cast<uint32_t*>(to_u + i * p.du.row_bytes) = b;
+      } else if (row0 + i < rows && !failed) {
+        st_codes4<0>(to_g + i * p.dg.row_bytes, cols - col, a);
+        st_codes4<0>(to_u + i * p.du.row_bytes, cols - col, b);
       }
     }
     if constexpr (TRANSPOSED) {
@@ -572,22 +622,25 @@ __global__ void __launch_bounds__(kF8BackThreads, 1)
         }
       }
       __syncthreads();
-      const int64_t at0 = rb * 128;
-      for (int i = threadIdx.x; i < 3 * 128 * 8; i += kF8BackThreads) {
-        const int which = i / (128 * 8), c = i / 8 % 128, piece = i % 8;
-        const int64_t at = at0 + 16 * piece;
-        if (col0 + c >= cols || at >= rows || failed) continue;
-        const int x = (c >> 2) & 15;
-        const uint4 two = *reinterpret_cast<const uint4*>(&sh.codes[which][c][(2 * piece ^ x) & ~1]);
-        const uint4 v = x & 1 ? make_uint4(two.z, two.w, two.x, two.y) : two;
-        const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
-        uint8_t* const o = t.data + (col0 + c) * t.row_bytes + at;
-        if (at + 16 <= rows) {
-          *reinterpret_cast<uint4*>(o) = v;
-        } else {
+      const int c0 = threadIdx.x / 8, piece = threadIdx.x % 8, x = (c0 >> 2) & 15;
+      const int64_t at = rb * 128 + 16 * piece;
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (at + k < rows) o[k] = (uint8_t)(vword(v, k / 4) >> (8 * (k % 4)));
+      for (int which = 0; which < 3; ++which) {
+        const F8View& t = which == 0 ? p.dg_t : which == 1 ? p.du_t : p.h_t;
+        uint8_t* const first = t.data + (col0 + c0) * t.row_bytes + at;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = c0 + 64 * k;  // (which leaves x as it is)
+          const uint4 two = *reinterpret_cast<const uint4*>(&sh.codes[which][c][(2 * piece ^ x) & ~1]);
+          const uint4 v = x & 1 ? make_uint4(two.z, two.w, two.x, two.y) : two;
+          uint8_t* const o = first + 64 * k * t.row_bytes;
+          if (whole || (col0 + c < cols && at + 16 <= rows && !failed)) {
+            *reinterpret_cast<uint4*>(o) = v;
+          } else if (col0 + c < cols && !failed) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (at + e < rows) o[e] = (uint8_t)(vword(v, e / 4) >> (8 * (e % 4)));
+          }
         }
       }
     }
