@@ -138,13 +138,13 @@ int tile_tokens(const F8Call& c) {
 // constants were fitted to 618 products (graph replays on GB300, inputs in L2:
 // 1..1024 tokens x 512..16384 columns x 512..7200, gated and not, every split).
 // Over these the choice takes 2 % longer than the best form in the geometric
-// mean, and 28 % at most (512 x 512 x 2048: 7.4 us, 5.8 in eight parts).
+// mean, and 25 % at most (512 x 512 x 2048: 7.2 us, 5.8 in eight parts).
 //
 // Narrow: waves of clusters, kClusters[s] of s CTAs of which the 152 SMs hold at
 // once, two CTAs an SM.  A block of K takes as long as its weights' way from L2,
 // or the sums' way through registers, more of either with a second CTA beside.
 //   tokens x columns x K        parts: 1     2     4     5     8    wide   (us)
-//   1 x 7168 x 7168              16.0   9.5   8.6   8.0  10.2   28.4
+//   1 x 7168 x 7168              16.0   9.5   8.6   8.0  10.2   27.6
 //   128 x 7168 x 7168            30.1  18.7  16.2  15.3  21.4   29.8
 //   333 x 2050 x 7200            30.9  19.1  15.8  14.7  19.2   29.6
 //   512 x 16384 x 1024           27.1  36.9  52.0  66.3  93.5   15.3

@@ -127,35 +127,38 @@ struct F8ProductMaps {
 // columns (part 0 or 1 of the tile's two blocks of columns) or, gated, of 64 of
 // the gate and the same 64 of the up-projection.
 //
-// The eight warps' way through a block bounds this more than the tensor cores
-// (515 clocks a block): a look at a barrier takes about 80 clocks, an arrival
-// 40, the loads of 64 columns 60 and their additions 70, one after the other.
-// So a block has one wait and one arrival, scales come for four blocks at a
-// time, and the loads of its second half are under way while the first half is
-// added.
+// The eight warps' way through a block bounds this, not the tensor cores, which
+// take 515 clocks for one (with the loads from TMEM and the additions taken out,
+// in a copy, 8192 x 7168 x 4096 took 142 us, with both 217, now 193): a look at a
+// barrier takes about 80 clocks, an arrival 40, the loads of 64 columns 60 and
+// their additions 70, one after the other, and code that is longer is fetched
+// more slowly (two blocks unrolled: 222 us).  So a block has one wait and one
+// arrival, scales come for four blocks at a time from two warps of their own, the
+// next loads are under way while columns are added, and the next block's barrier
+// is looked at meanwhile.  Tried and not kept: accumulators of 128 columns, four
+// in turn (244 us); sixteen warps of 64 columns (214); 16 columns at a time (304).
 struct F8WideCfg {
   static constexpr int TM = 256, TN = 256;
   static constexpr uint32_t A_BYTES = 128 * 128, W_BYTES = 128 * 128, STAGE = A_BYTES + W_BYTES;
   static constexpr int STAGES = 6;
-  // Scales, a ring of groups of four blocks of K.  w with block scales: for each
-  // of the tile's two blocks of columns and each row the products of their
-  // scales, four together.  w with row scales: the rows' scales, four together,
-  // then block by block those of 256 columns.
+  // Scales, a ring of groups of four blocks of K, each made by a warp of its own:
+  // for each block the products of the rows' scales and those of the tile's two
+  // blocks of columns (128 each) or, w with row scales, the rows' scales and
+  // those of 256 columns.
   static constexpr int GROUP = 4, SF_RING = 2;
-  template <bool ROWS_W>
-  struct Sf {
-    static constexpr uint32_t COLUMNS = 128 * 16;  // behind the rows' (ROWS_W)
-    static constexpr uint32_t BYTES = ROWS_W ? COLUMNS + GROUP * TN * 4 : 2 * 128 * 16;
-  };
-  static constexpr uint32_t SMEM = STAGES * STAGE + SF_RING * Sf<true>::BYTES + 1024;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr uint32_t SF_BLOCK = (128 + TN) * 4, SF_BYTES = GROUP * SF_BLOCK;
+  static constexpr uint32_t SMEM = STAGES * STAGE + SF_RING * SF_BYTES + 1024;
+  static constexpr int PARTS = 2;        // warps that share a row
+  static constexpr int CW = TN / PARTS;  // a thread's columns
+  static constexpr int CH = CW / 4;      // of them at a time
+  static constexpr int EPI_WARPS = 4 * PARTS;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int ACCS = 2, ACC_COLS = 256, COLS = ACCS * ACC_COLS;
   // registers: 168 a thread at launch, 64512 in all, of which the first
-  // warpgroup gives 96 a thread to the other two
-  static constexpr int REGS_FEW = 72, REGS_MANY = 216;
-  static_assert(128 * REGS_FEW + 256 * REGS_MANY <= 168 * THREADS, "the split of the registers");
-  static_assert(SMEM <= 227 * 1024 && SF_RING == 2, "shared memory; the ring's turns below");
+  // warpgroup gives 112 a thread to the other two
+  static constexpr int REGS_FEW = 56, REGS_MANY = 224;
+  static_assert(128 * REGS_FEW + 32 * EPI_WARPS * REGS_MANY <= 168 * THREADS, "the split of the registers");
+  static_assert(SMEM <= 227 * 1024 && SF_RING == 2, "shared memory; a slot of the ring for each of two warps");
 };
 
 // N bf16 columns of a lane's row, `left` of which exist; `whole`: every row
@@ -199,22 +202,22 @@ __device__ __forceinline__ void store_f32(float* o, const f32x2* v, int left, bo
   }
 }
 
-// 64 values of a lane's row in codes, over the scale of all 128 columns of the
-// row, whose other half another warp holds: `other` gives the bits of the amax
-// of both.  Columns behind the last hold 0 (or, with their whole row, NaN).
-template <class Other>
+// N values of a lane's row in codes, over the scale of all 128 columns of the
+// row, whose other parts other warps hold: `other` gives the bits of the amax of
+// them all.  Columns behind the last hold 0 (or, with their whole row, NaN).
+template <int N, class Other>
 __device__ __forceinline__ void store_f8(const F8View& q, int64_t row, int64_t col, bool stores, const f32x2* v,
                                          Other other) {
   float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) m = amax3(m, v[k]);
+  for (int k = 0; k < N / 2; ++k) m = amax3(m, v[k]);
   const F8Scale s = f8_scale(other(__float_as_uint(m)));
   if (!stores || row >= q.rows) return;
   if (col % kF8Block == 0) q.scales[col / kF8Block * q.scales_row + row] = s.by;
   uint8_t* const o = q.data + row * q.row_bytes + col;
   const int64_t left = q.cols - col;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < N / 16; ++k) {
     uint32_t c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = f8_codes(v[8 * k + 2 * j], v[8 * k + 2 * j + 1], s);
@@ -234,12 +237,11 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
                             const __grid_constant__ F8ProductMaps maps) {
   using C = F8WideCfg;
   constexpr int S = C::STAGES, R = C::SF_RING, A = C::ACCS;
-  using Sf = typename C::template Sf<ROWS_W>;
   constexpr bool GATED = OUT == kF8GatedCodes || OUT == kF8GatedBf16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) unsigned long long bars[2 * S + 2 * A + 1 + 2 * R];
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t xch[2][2][128];  // [turn][part][row]: amaxes of the warps that share a row
+  __shared__ uint32_t xch[2][C::PARTS][128];  // [turn][part][row]: amaxes of the warps that share a row
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -330,52 +332,55 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
         (void)phase_wait(drained, 0);
         drain_stages<S>(full, s, use);
       }
-    } else if (warp == 2) {
+    } else if (warp >= 2) {
       bool failed = false;
       uint32_t group = 0;
+      const uint32_t r = warp - 2, slot = sf_at + r * C::SF_BYTES + 16 * lane;
       for (int i = first; i < tiles && !failed; i += step) {
         int mt, nt;
         tile_at(walk, i, mt, nt);
         const int64_t row = (int64_t)mt * C::TM + rank * 128 + 4 * lane, col = (int64_t)nt * C::TN + 4 * lane;
         for (int k4 = 0; k4 < blocks; k4 += C::GROUP, ++group) {
-          float a[4][4], w[4][ROWS_W ? 8 : 2];  // [block]; 1 behind the last
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = k4 + j;
-            const bool one = k < blocks0;
-            const int64_t kb = one ? k : k - blocks0;
-            const F8Scales& sa = p.a[one ? 0 : 1];
-            const F8Scales& sw = p.w[one ? 0 : 1];
-            ld_scales4(sa.at + kb * sa.row, row, k < blocks ? p.m : 0, a[j]);
-            if constexpr (ROWS_W) {
-              ld_scales4(sw.at + kb * sw.row, col, k < blocks ? p.n : 0, &w[j][0]);
-              ld_scales4(sw.at + kb * sw.row, col + 128, k < blocks ? p.n : 0, &w[j][4]);
-            } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const F8Scales& sh = GATED ? p.w[h] : sw;
-                const int64_t at = GATED ? nt : 2 * (int64_t)nt + h;
-                w[j][h] = k < blocks && at * 128 < p.n ? sh.at[at * sh.row + kb] : 1.f;
-              }
-            }
-          }
-          const uint32_t r = group % R, slot = sf_at + r * Sf::BYTES;
+          if (group % R != r) continue;
           if (group >= R) phase_or_flag(sf_empty + 8 * r, (group / R - 1) & 1, failed, p.err, kErrStageTimeout);
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
+#pragma unroll 1
+          for (int j2 = 0; j2 < C::GROUP && k4 + j2 < blocks; j2 += 2) {  // the loads of two blocks together
+            float a[2][4], w[2][ROWS_W ? 8 : 2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t at = slot + 16 * (4 * lane + e);
-            if constexpr (ROWS_W) {
-              st_shared4(at, a[0][e], a[1][e], a[2][e], a[3][e]);
+            for (int j = 0; j < 2; ++j) {
+              const int k = k4 + j2 + j;
+              const bool one = k < blocks0, in = k < blocks;
+              const int64_t kb = one ? k : k - blocks0;
+              const F8Scales& sa = p.a[one ? 0 : 1];
+              const F8Scales& sw = p.w[one ? 0 : 1];
+              ld_scales4(sa.at + kb * sa.row, row, in ? p.m : 0, a[j]);
+              if constexpr (ROWS_W) {
+                ld_scales4(sw.at + kb * sw.row, col, in ? p.n : 0, &w[j][0]);
+                ld_scales4(sw.at + kb * sw.row, col + 128, in ? p.n : 0, &w[j][4]);
+              } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                st_shared4(slot + Sf::COLUMNS + C::TN * 4 * e + 512 * h + 16 * lane, w[e][4 * h], w[e][4 * h + 1],
-                           w[e][4 * h + 2], w[e][4 * h + 3]);
-            } else {
+                for (int h = 0; h < 2; ++h) {
+                  const F8Scales& sh = GATED ? p.w[h] : sw;
+                  const int64_t at = GATED ? nt : 2 * (int64_t)nt + h;
+                  w[j][h] = in && at * 128 < p.n ? sh.at[at * sh.row + kb] : 1.f;
+                }
+              }
+            }
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                st_shared4(at + 128 * 16 * h, a[0][e] * w[0][h], a[1][e] * w[1][h], a[2][e] * w[2][h], a[3][e] * w[3][h]);
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t at = slot + (j2 + j) * C::SF_BLOCK;
+              if constexpr (ROWS_W) {
+                st_shared4(at, a[j][0], a[j][1], a[j][2], a[j][3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  st_shared4(at + 512 + 512 * h, w[j][4 * h], w[j][4 * h + 1], w[j][4 * h + 2], w[j][4 * h + 3]);
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  st_shared4(at + 512 * h, a[j][0] * w[j][h], a[j][1] * w[j][h], a[j][2] * w[j][h], a[j][3] * w[j][h]);
+              }
             }
           }
           __syncwarp();
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MANY));
     bool failed = false;
     const int q = warp % 4, part = (warp - 4) / 4;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + (GATED ? 64 : 128) * part;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + (GATED ? C::CW / 2 : C::CW) * part;
     const uint32_t release = map_rank(acc_empty, 0);
     // whole sectors: every row starts on a 32-byte boundary
     const bool wide = p.out_row % (OUT == kF8OutF32 ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
@@ -398,9 +403,9 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
       int mt, nt;
       tile_at(walk, i, mt, nt);
       const int64_t row = (int64_t)mt * C::TM + rank * 128 + 32 * q + lane;
-      f32x2 sum[64];
+      f32x2 sum[C::CW / 2];
 #pragma unroll
-      for (int e = 0; e < 64; ++e) sum[e] = f2_make(0.f, 0.f);
+      for (int e = 0; e < C::CW / 2; ++e) sum[e] = f2_make(0.f, 0.f);
       // A wait is one look in the common case, and nothing else lies on the way.
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (phase_done(bar, parity) || failed) return;
@@ -409,12 +414,13 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
           atomicOr(p.err, kErrStageTimeout);
         }
       };
-      // this row's factors in a group of scales (gated: gate's, and behind them up's)
-      const uint32_t mine = sf_at + 16 * (32 * q + lane) + (ROWS_W || GATED ? 0 : 128 * 16 * part);
-      uint32_t v[2][32];
+      // this row's factors of a block (gated: gate's, and behind them up's)
+      const uint32_t mine = sf_at + 4 * (32 * q + lane) + (ROWS_W || GATED ? 0 : 512 * (C::CW * part / 128));
+      uint32_t v[2][C::CH];
       float f[2], f_next[2];
       auto load = [&](uint32_t block, int piece) {
-        tmem_ld(lanes + (block & 1) * C::ACC_COLS + (GATED ? 128 * (piece / 2) + 32 * (piece % 2) : 32 * piece), v[piece % 2]);
+        tmem_ld(lanes + (block & 1) * C::ACC_COLS + (GATED ? 128 * (piece / 2) + C::CH * (piece % 2) : C::CH * piece),
+                v[piece % 2]);
       };
       auto loaded = [&]() {
         tmem_ld_wait(v[0]);
@@ -422,9 +428,9 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
       };
       auto factors = [&](uint32_t in_group) {
         if (in_group == 0) wait(sf_full + 8 * (group & 1), (group >> 1) & 1);
-        const uint32_t at = mine + (group & 1) * Sf::BYTES + 4 * in_group;
+        const uint32_t at = mine + (group & 1) * C::SF_BYTES + in_group * C::SF_BLOCK;
         f_next[0] = ld_shared(at);
-        f_next[1] = GATED ? ld_shared(at + 128 * 16) : f_next[0];
+        f_next[1] = GATED ? ld_shared(at + 512) : f_next[0];
       };
       if (blocks > 0) {
         factors(0);
@@ -438,20 +444,21 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
       for (int k = 0; k < blocks; ++k) {
         const uint32_t in_group = k % C::GROUP;
         const bool last = k == blocks - 1, leaves = in_group == C::GROUP - 1 || last;
-        const uint32_t columns = sf_at + (group & 1) * Sf::BYTES + Sf::COLUMNS + C::TN * 4 * in_group + 512 * part;
+        const uint32_t columns = sf_at + (group & 1) * C::SF_BYTES + in_group * C::SF_BLOCK + 512 + 4 * C::CW * part;
         f[0] = f_next[0];
         f[1] = f_next[1];
         auto add = [&](int piece) {
           const f32x2 by = f2_make(f[piece / 2], f[piece / 2]);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
+          for (int e = 0; e < C::CH / 2; e += 2) {
             f32x2 s[2] = {};
-            if constexpr (ROWS_W) ld_shared_pairs(columns + 128 * piece + 8 * e, s);
+            if constexpr (ROWS_W) ld_shared_pairs(columns + 4 * C::CH * piece + 8 * e, s);
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
               const uint32_t* const x = &v[piece % 2][2 * (e + o)];
               const f32x2 y = f2_make(__uint_as_float(x[0]), __uint_as_float(x[1]));
-              sum[16 * piece + e + o] = f2_fma(y, ROWS_W ? f2_mul(s[o], by) : by, sum[16 * piece + e + o]);
+              f32x2& to = sum[C::CH / 2 * piece + e + o];
+              to = f2_fma(y, ROWS_W ? f2_mul(s[o], by) : by, to);
             }
           }
         };
@@ -497,8 +504,8 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
       if (i + step >= tiles) grid_dep_launch_dependents();
       if constexpr (!GATED) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t col = (int64_t)nt * C::TN + 128 * part + 64 * h;
+        for (int h = 0; h < C::CW / 64; ++h) {
+          const int64_t col = (int64_t)nt * C::TN + C::CW * part + 64 * h;
           if (failed || row >= p.m || col >= p.n) continue;
           const int left = (int)(p.n - col < 64 ? p.n - col : 64);
           if constexpr (OUT == kF8OutBf16)
@@ -507,28 +514,30 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
             store_f32<64>(static_cast<float*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide, p.add);
         }
       } else {
-        const int64_t col = (int64_t)nt * 128 + 64 * part;
-        // the amax of this row's values and the other part's
+        constexpr int N = C::CW / 2;
+        const int64_t col = (int64_t)nt * 128 + N * part;
+        // the amax of this row's values and the other parts'
         auto other = [&](uint32_t m) {
-          uint32_t(&x)[2][128] = xch[turn++ & 1];
+          uint32_t(&x)[C::PARTS][128] = xch[turn++ & 1];
           x[part][32 * q + lane] = m;
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
-          return max(m, x[1 - part][32 * q + lane]);
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + q), "n"(32 * C::PARTS) : "memory");
+#pragma unroll
+          for (int o = 1; o < C::PARTS; ++o) m = max(m, x[(part + o) % C::PARTS][32 * q + lane]);
+          return m;
         };
         const bool stores = !failed && col < p.n;
-        if (p.g.data) store_f8(p.g, row, col, stores, sum, other);
-        if (p.u.data) store_f8(p.u, row, col, stores, sum + 32, other);
+        if (p.g.data) store_f8<N>(p.g, row, col, stores, sum, other);
+        if (p.u.data) store_f8<N>(p.u, row, col, stores, sum + N / 2, other);
         f32x2* const h = sum;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < N / 2; ++e) {
           const float lo = f8_act<ACT>(f2_lo(h[e])), hi = f8_act<ACT>(f2_hi(h[e]));
-          h[e] = f2_mul(f2_make(lo, hi), h[32 + e]);
+          h[e] = f2_mul(f2_make(lo, hi), h[N / 2 + e]);
         }
         if constexpr (OUT == kF8GatedCodes) {
-          store_f8(p.h, row, col, stores, h, other);
+          store_f8<N>(p.h, row, col, stores, h, other);
         } else if (stores && row < p.m) {
-          store_bf16<64>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, h,
-                         (int)(p.n - col < 64 ? p.n - col : 64), wide);
+          store_bf16<N>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, h, (int)(p.n - col < N ? p.n - col : N), wide);
         }
       }
     }
