@@ -209,6 +209,20 @@ def test_refusals(lib, call, change, status):
     assert call(**change) == status
 
 
+@pytest.mark.parametrize("call", [matmul, gated])
+def test_forms(lib, call):
+    big = dict(a=matrix(1, cols=4096), w=matrix(2, SQUARE, rows=70, cols=4096)) if call is matmul else dict(
+        x=matrix(1, cols=4096), gate=matrix(2, SQUARE, rows=72, cols=4096), up=matrix(3, SQUARE, rows=72, cols=4096))
+    K, S = ar.FLAG_KERNEL, ar.FLAG_SPLIT
+    for flags in (K(3), S(1), K(2) | S(1), K(1) | S(3), ar.FLAG_STAGES(2), ar.FLAG_TP_GRAM):
+        assert call(flags=flags) == 1  # (two blocks of K)
+    assert call(flags=K(1) | S(9), **big) == 1
+    if not torch.cuda.is_available():
+        for flags in (K(1), K(2), K(1) | S(2), K(1) | ar.FLAG_PDL):
+            assert call(flags=flags) in (4, 5)
+        assert call(flags=K(1) | S(8), **big) in (4, 5)
+
+
 def test_nothing_to_write_is_a_no_op(lib):
     assert quantize(matrix(1, rows=0, data=0), x=0) == 0
     assert quantize(matrix(1, cols=0, data=0), x=0) == 0
