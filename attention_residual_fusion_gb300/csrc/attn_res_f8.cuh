@@ -24,7 +24,6 @@ struct F8View {
 
 __host__ __device__ constexpr int64_t f8_blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
 
-
 // max(m, |a|, |b|), a NaN if there is one (its bits are then above infinity's).
 __device__ __forceinline__ float amax3(float m, f32x2 v) {
   float r;
@@ -38,8 +37,8 @@ __device__ __forceinline__ float warp_amax(float m) {
   return __uint_as_float(r);
 }
 
-// A group's scale from the bits of its amax, and what its codes are made with:
-// its correctly rounded inverse and whether quotients may be taken with it.
+// A group's scale from the bits of its amax, and its inverse, which codes are
+// made with; both correctly rounded, NaN where the amax is no finite number.
 struct F8Scale {
   float by, inverse;
 };
@@ -78,7 +77,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return w;
 }
-// Codes of four values over one scale that is a number.
+// Codes of four values over one scale that is a number (within
+// f8_quotients_held those of the correctly rounded quotient).
 __device__ __forceinline__ uint32_t f8_codes(f32x2 lo, f32x2 hi, float by, float inverse) {
   const f32x2 b = f2_make(by, by), r = f2_make(-inverse, -inverse);
   const f32x2 x = f8_negated_quotient2(lo, b, r), y = f8_negated_quotient2(hi, b, r);
@@ -105,10 +105,12 @@ __device__ __forceinline__ f32x2 e4m3_pair(uint32_t codes) {
 // ---- activations -------------------------------------------------------------------------
 
 // act(g) = g / (1 + exp(-z)) with z = g (SiLU) or 2 sqrt(2 / pi) (g + 0.044715
-// g^3) (GELU in its tanh form: (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y))).  The
-// fast exponential is off by up to 2^-16 of itself (near |z| = 88, by a few
-// units of 2^-23 for small z), the fast reciprocal by one; from z = -88.7 down
-// the exponential is infinite and act(g) 0.
+// g^3) (GELU in its tanh form: (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y))).
+//
+// The products' epilogue takes the fast exponential (f8_sigmoid), off by up to
+// 2^-16 of itself near |z| = 88 and by a few units of 2^-23 for small z; from z =
+// -88.7 down the exponential is infinite and act(g) 0.  The backward pass, whose
+// gradients are compared with differences, has it to a few units (f8_sigmoid2).
 constexpr float kGeluScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 

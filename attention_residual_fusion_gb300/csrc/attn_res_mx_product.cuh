@@ -21,6 +21,7 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t tmem, uint64_t desc) {
   else
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
+
 #define ATTN_RES_MMA_SCALED(GROUP, KIND)                                                         \
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                                 \
                "tcgen05.mma.cta_group::" #GROUP ".kind::" KIND                                   \

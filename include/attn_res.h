@@ -469,11 +469,14 @@ attn_res_status_t attn_res_mx_matmul(const attn_res_mx_t* a, const attn_res_mx_t
  *   code = rn_e4m3(x / s), saturating at +-448
  * (fp32 quotients, correctly rounded; rn: to nearest, ties to even).  A group
  * that holds a NaN or an infinity gets the scale NaN and zero codes: it stands
- * for NaN throughout.  Scales that a caller makes may be any fp32 values.
+ * for NaN throughout.  Scales that a caller makes may be any fp32 values.  So
+ * attn_res_f8_quantize, to the bit; results that attn_res_f8_gated and its
+ * backward make in codes come from fp32 values that carry roundings of their
+ * own, and their x / s may be off by two units of its last place more.
  *
  * Data: element k of row r is the byte data[r * row_bytes + k].  Any number of
- * columns; data 16-byte aligned and row_bytes a multiple of 16 (for one row: at
- * least cols).  Bytes past a row's last are neither read nor written.
+ * columns; data 16-byte aligned, row_bytes a multiple of 16 and at least cols.
+ * Bytes past a row's last are neither read nor written.
  * Scales, with b = k / 128:
  *   ATTN_RES_F8_ROWS    scales[b * scales_row + r]: blocks of columns outermost,
  *                       scales_row >= rows and a multiple of 4, 16-byte aligned;
@@ -561,7 +564,8 @@ attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t
  * activation: ATTN_RES_SILU, act(g) = g / (1 + exp(-g)), or ATTN_RES_GELU, the
  * tanh form g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, as g / (1 +
  * exp(-z)) too.  (Fast exponential: act(g) to 2^-16 of itself where it is small,
- * to a few 2^-23 elsewhere; 0 where exp(-z) overflows, below z = -88.7.)
+ * to a few 2^-23 elsewhere; 0 where exp(-z) overflows, below z = -88.7.  The
+ * backward pass has 1 / (1 + exp(-z)) of its fp32 z to a few 2^-23 throughout.)
  */
 #define ATTN_RES_SILU 1
 #define ATTN_RES_GELU 2
