@@ -261,6 +261,9 @@ attn_res_status_t attn_res_f8_gated_backward(const attn_res_bf16_t* dh, int64_t 
   for (const attn_res_f8_t* q : {g, u, dg, du, dg_t, du_t, h_t})
     if (st == ATTN_RES_OK && q != nullptr) st = check_matrix(*q);
   if (st != ATTN_RES_OK) return st;
+  // (these are read through tensor maps, which hold strides below 2^40 bytes)
+  if (dh_row * 2 >= kMaxStride || g->scales_row * 4 >= kMaxStride || u->scales_row * 4 >= kMaxStride)
+    return ATTN_RES_EINVAL;
   Spans<15> spans;
   spans.add(rows_span(dh, T, dh_row, F, false));
   for (const attn_res_f8_t* q : {g, u}) spans.add(q, false);

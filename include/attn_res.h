@@ -585,6 +585,7 @@ attn_res_status_t attn_res_f8_gated(const attn_res_f8_t* x, const attn_res_f8_t*
  * up (attn_res_f8_matmul of them and the transposed weights); and, if not NULL
  * (all three or none), the transposed dg_t, du_t and h_t [F, T], quantised by
  * themselves in groups along the tokens, for the gradients of the weights.
+ * Rows of dh, and of g's and u's scales, lie less than 2^40 bytes apart.
  */
 attn_res_status_t attn_res_f8_gated_backward(const attn_res_bf16_t* dh, int64_t dh_row,
                                              const attn_res_f8_t* g, const attn_res_f8_t* u,
