@@ -188,6 +188,7 @@ attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t
   spans.add(a2, false);
   spans.add(w2, false);
   if (spans.clash()) return ATTN_RES_EALIAS;
+  if (!f8_choose_form(&c)) return ATTN_RES_EINVAL;
   st = current_device(&c.device);
   if (st != ATTN_RES_OK) return st;
   cudaError_t e = device_status_word(c.device, &c.err);
@@ -229,6 +230,7 @@ attn_res_status_t attn_res_f8_gated(const attn_res_f8_t* x, const attn_res_f8_t*
   for (const attn_res_f8_t* q : {h, save_g, save_u}) spans.add(q, true);
   spans.add(rows_span(h_rows, T, h_row, F, true));
   if (spans.clash()) return ATTN_RES_EALIAS;
+  if (!f8_choose_form(&c)) return ATTN_RES_EINVAL;
   st = current_device(&c.device);
   if (st != ATTN_RES_OK) return st;
   cudaError_t e = device_status_word(c.device, &c.err);

@@ -23,8 +23,12 @@ struct F8Call {
   unsigned* err;
   cudaStream_t stream;
 };
-cudaError_t launch_f8_product(const F8Call& c);
 // Whether the overrides can be met.
 bool f8_overrides_ok(const F8Call& c);
+// Chooses what is automatic of form and split; false where the wide form would
+// have more tiles than it counts (results beyond any device's memory).
+bool f8_choose_form(F8Call* c);
+// Of a call with its form chosen.
+cudaError_t launch_f8_product(const F8Call& c);
 
 }  // namespace attn_res_host

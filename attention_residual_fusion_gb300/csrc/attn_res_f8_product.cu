@@ -76,6 +76,13 @@ cudaError_t product_maps(const F8Call& c, uint32_t a_rows, F8ProductMaps* maps) 
   return e;
 }
 
+// Tiles of the wide form's walk, rows of `a` and columns.
+int64_t wide_m_tiles(const F8Call& c) { return (c.a->rows + F8WideCfg::TM - 1) / F8WideCfg::TM; }
+int64_t wide_n_tiles(const F8Call& c) {
+  const int64_t columns = c.gated ? 128 : F8WideCfg::TN;
+  return (c.w->rows + columns - 1) / columns;
+}
+
 template <int OUT, int ACT, bool ROWS_W>
 struct Wide {
   using C = F8WideCfg;
@@ -101,10 +108,7 @@ struct Wide {
     F8ProductMaps maps = {};
     if (e == cudaSuccess) e = product_maps(c, 128, &maps);
     if (e != cudaSuccess) return e;
-    const int64_t columns = c.gated ? 128 : C::TN;
-    const int64_t m_tiles = (c.a->rows + C::TM - 1) / C::TM, n_tiles = (c.w->rows + columns - 1) / columns;
-    const int64_t tiles = m_tiles * n_tiles;
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const int64_t m_tiles = wide_m_tiles(c), n_tiles = wide_n_tiles(c), tiles = m_tiles * n_tiles;
     const TileWalk walk{(int)m_tiles, (int)n_tiles};
     Attributes l(dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs), 1, 1), C::THREADS, C::SMEM, 2, c.stream);
     return cudaLaunchKernelEx(&l.cfg, kern, params(c), walk, maps);
@@ -178,8 +182,7 @@ int64_t plan_narrow(const F8Call& c, int64_t blocks, int* split) {
 }
 // Wide: waves of pairs.
 int64_t wide_cost(const F8Call& c, int64_t blocks) {
-  const int64_t columns = c.gated ? 128 : 256;
-  const int64_t tiles = (c.a->rows + 255) / 256 * ((c.w->rows + columns - 1) / columns);
+  const int64_t tiles = wide_m_tiles(c) * wide_n_tiles(c);
   return 1630 + (tiles + kSms / 2 - 1) / (kSms / 2) * (3190 + (c.w->block == ATTN_RES_F8_ROWS ? 820 : 471) * blocks);
 }
 
@@ -206,13 +209,18 @@ bool f8_overrides_ok(const F8Call& c) {
   return c.a->rows <= narrow_max_rows(c) && c.split <= kF8MaxSplit && (c.split <= 1 || c.split <= k_blocks(c));
 }
 
-cudaError_t launch_f8_product(const F8Call& call) {
-  F8Call c = call;
-  const bool rows = c.w->block == ATTN_RES_F8_ROWS;
+bool f8_choose_form(F8Call* call) {
+  F8Call& c = *call;
   if (c.kernel != ATTN_RES_F8_WIDE && c.split == 0 && c.a->rows <= narrow_max_rows(c)) {
     const int64_t blocks = k_blocks(c), narrow = plan_narrow(c, blocks, &c.split);
     if (c.kernel == 0 && narrow <= wide_cost(c, blocks)) c.kernel = ATTN_RES_F8_NARROW;
   }
+  if (c.kernel == 0) c.kernel = ATTN_RES_F8_WIDE;
+  return c.kernel == ATTN_RES_F8_NARROW || wide_m_tiles(c) * wide_n_tiles(c) <= INT32_MAX / 2;
+}
+
+cudaError_t launch_f8_product(const F8Call& c) {
+  const bool rows = c.w->block == ATTN_RES_F8_ROWS;
   if (c.kernel == ATTN_RES_F8_NARROW) {
     if (c.gated) return launch_narrow<true, false>(c, c.split);
     return rows ? launch_narrow<false, true>(c, c.split) : launch_narrow<false, false>(c, c.split);
