@@ -111,6 +111,8 @@ __device__ __forceinline__ f32x2 e4m3_pair(uint32_t codes) {
 // 2^-16 of itself near |z| = 88 and by a few units of 2^-23 for small z; from z =
 // -88.7 down the exponential is infinite and act(g) 0.  The backward pass, whose
 // gradients are compared with differences, has it to a few units (f8_sigmoid2).
+// GELU's z comes with up to three (backward: two) units of roundings of its own,
+// which exp(-z) takes |z| times: 2^-16 more near |z| = 88 on random gates.
 constexpr float kGeluScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 

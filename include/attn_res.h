@@ -563,9 +563,10 @@ attn_res_status_t attn_res_f8_matmul(const attn_res_f8_t* a, const attn_res_f8_t
  * attn_res_f8_gated_backward takes.
  * activation: ATTN_RES_SILU, act(g) = g / (1 + exp(-g)), or ATTN_RES_GELU, the
  * tanh form g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, as g / (1 +
- * exp(-z)) too.  (Fast exponential: act(g) to 2^-16 of itself where it is small,
- * to a few 2^-23 elsewhere; 0 where exp(-z) overflows, below z = -88.7.  The
- * backward pass has 1 / (1 + exp(-z)) of its fp32 z to a few 2^-23 throughout.)
+ * exp(-z)) too.  (Fast exponential: act(g) to 2^-16 of itself where it is small
+ * -- GELU's, whose z carries fp32 roundings of its own, to 2^-14 --, to a few
+ * 2^-23 elsewhere; 0 where exp(-z) overflows, below z = -88.7.  The backward pass
+ * has 1 / (1 + exp(-z)) of its fp32 z to a few 2^-23 throughout.)
  */
 #define ATTN_RES_SILU 1
 #define ATTN_RES_GELU 2
