@@ -82,12 +82,6 @@ __device__ __forceinline__ float ld_shared(uint32_t at) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
-
-__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
-}
 __device__ __forceinline__ void ld_shared_pairs(uint32_t at, f32x2 (&v)[2]) {
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(at) : "memory");
 }
@@ -161,14 +155,13 @@ struct F8WideCfg {
   static_assert(SMEM <= 227 * 1024 && SF_RING == 2, "shared memory; a slot of the ring for each of two warps");
 };
 
-// N bf16 columns of a lane's row, `left` of which exist; `whole`: every row
+// 64 bf16 columns of a lane's row, `left` of which exist; `whole`: every row
 // starts on a 32-byte boundary.
-template <int N>
 __device__ __forceinline__ void store_bf16(uint16_t* o, const f32x2* x, int left, bool whole) {
-  uint32_t v[N / 2];
+  uint32_t v[32];
 #pragma unroll
-  for (int e = 0; e < N / 2; ++e) v[e] = pack_bf16x2(f2_lo(x[e]), f2_hi(x[e]));
-  store_row<N>(o, v, left, whole);
+  for (int e = 0; e < 32; ++e) v[e] = pack_bf16x2(f2_lo(x[e]), f2_hi(x[e]));
+  store_row(o, v, left, whole);
 }
 // N fp32 columns; `add`: to what is there.
 template <int N>
@@ -510,7 +503,7 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
           if (failed || row >= p.m || col >= p.n) continue;
           const int left = (int)(p.n - col < 64 ? p.n - col : 64);
           if constexpr (OUT == kF8OutBf16)
-            store_bf16<64>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide);
+            store_bf16(static_cast<uint16_t*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide);
           else
             store_f32<64>(static_cast<float*>(p.out) + row * p.out_row + col, sum + 32 * h, left, wide, p.add);
         }
@@ -538,7 +531,7 @@ __global__ void __launch_bounds__(F8WideCfg::THREADS, 1)
         if constexpr (OUT == kF8GatedCodes) {
           store_f8<N>(p.h, row, col, stores, h, other);
         } else if (stores && row < p.m) {
-          store_bf16<N>(static_cast<uint16_t*>(p.out) + row * p.out_row + col, h, (int)(p.n - col < N ? p.n - col : N), wide);
+          store_bf16(static_cast<uint16_t*>(p.out) + row * p.out_row + col, h, (int)(p.n - col < N ? p.n - col : N), wide);
         }
       }
     }

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(WideCfg<FMT, HALVES>::THREADS, 1)
       int local[2] = {};
       auto store = [&](int h) {
         const int col = nt * C::TN + local[h];
-        store_row<64>(p.out + row * p.out_row + col, v[h], (int)p.n - col, wide);
+        store_row(p.out + row * p.out_row + col, v[h], (int)p.n - col, wide);
       };
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

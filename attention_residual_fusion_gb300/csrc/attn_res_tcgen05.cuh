@@ -169,8 +169,8 @@ __device__ __forceinline__ void pack64(const uint32_t (&r)[64], float scale, uin
     v[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
 }
 // COUNT of them from FIRST on, `left` of which exist.
-template <int FIRST, int COUNT, int N>
-__device__ __forceinline__ void store_piece(uint16_t* o, const uint32_t (&v)[N], int left) {
+template <int FIRST, int COUNT>
+__device__ __forceinline__ void store_piece(uint16_t* o, const uint32_t (&v)[32], int left) {
   uint16_t* const at = o + FIRST;
   constexpr int k = FIRST / 2;
   if (left >= FIRST + COUNT) {
@@ -187,7 +187,7 @@ __device__ __forceinline__ void store_piece(uint16_t* o, const uint32_t (&v)[N],
   }
 }
 
-// Stores N columns (32 or 64) of a lane's row, `left` of which exist, straight from its
+// Stores 64 columns of a lane's row, `left` of which exist, straight from its
 // registers: 32 bytes, a whole sector, at a time, after half a sector where the
 // row lies between two of them; `wide`: none of the rows does, which a full
 // tile then need not look at (2 % of a product's time).  (Half sectors alone: 1361 x 14008 x 864 mxfp8
@@ -195,29 +195,23 @@ __device__ __forceinline__ void store_piece(uint16_t* o, const uint32_t (&v)[N],
 // bytes pass shared memory twice, whose bandwidth the operands need: 4096 x
 // 16384 x 2048 nvfp4 61 us instead of 56, 8192 x 7168 x 7168 mxfp4 115 either
 // way.)
-template <int N>
-__device__ __forceinline__ void store_row(uint16_t* o, const uint32_t (&v)[N / 2], int left, bool wide) {
-  static_assert(N == 32 || N == 64, "");
+__device__ __forceinline__ void store_row(uint16_t* o, const uint32_t (&v)[32], int left, bool wide) {
   auto sectors = [&](int exist) {
     store_piece<0, 16>(o, v, exist);
     store_piece<16, 16>(o, v, exist);
-    if constexpr (N == 64) {
-      store_piece<32, 16>(o, v, exist);
-      store_piece<48, 16>(o, v, exist);
-    }
+    store_piece<32, 16>(o, v, exist);
+    store_piece<48, 16>(o, v, exist);
   };
-  if (wide && left >= N) {
-    sectors(N);
+  if (wide && left >= 64) {
+    sectors(64);
   } else if ((reinterpret_cast<uintptr_t>(o) & 16u) == 0) {
     sectors(left);
   } else {
     store_piece<0, 8>(o, v, left);
     store_piece<8, 16>(o, v, left);
-    if constexpr (N == 64) {
-      store_piece<24, 16>(o, v, left);
-      store_piece<40, 16>(o, v, left);
-    }
-    store_piece<N - 8, 8>(o, v, left);
+    store_piece<24, 16>(o, v, left);
+    store_piece<40, 16>(o, v, left);
+    store_piece<56, 8>(o, v, left);
   }
 }
 
