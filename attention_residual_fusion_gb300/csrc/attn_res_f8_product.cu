@@ -139,10 +139,15 @@ int tile_tokens(const F8Call& c) {
 }
 
 // The choice of form and split: each one's time by a model of it, in ns, whose
-// constants were fitted to 618 products (graph replays on GB300, inputs in L2:
-// 1..1024 tokens x 512..16384 columns x 512..7200, gated and not, every split).
-// Over these the choice takes 2 % longer than the best form in the geometric
-// mean, and 25 % at most (512 x 512 x 2048: 7.2 us, 5.8 in eight parts).
+// constants were fitted to 79 products (45 with block scales, 6 with row scales on
+// both sides, 28 gated; 1..1024 tokens x 512..16384 columns x 512..7200; each in
+// the wide form and the narrow one's splits; graph replays on GB300, inputs in L2).
+// Over these the choice takes 2.4 % longer than the best form in the geometric
+// mean, and 25 % at most (512 x 512 x 2048: 8.0 us in eight parts, 6.4 in six).  Over 96
+// others, drawn at random (1..1400 x 128..12000 x 256..8000, 24 of each kind): block
+// scales 3.6 % (18 % at most), gated 1.6 % (17 %), row scales 0.8 % (13 %; the narrow
+// form's second multiplication is not in its model), sums of two products, which
+// were not fitted, 2.0 % (33 %, 872 x 324 x 3012 twice: 12.0 us in seven parts, 9.0 in six).
 //
 // Narrow: waves of clusters, kClusters[s] of s CTAs of which the 152 SMs hold at
 // once, two CTAs an SM.  A block of K takes as long as its weights' way from L2,

@@ -113,20 +113,24 @@ struct F8ProductMaps {
 // A pair of CTAs (cta_group::2) makes 256 tokens x 256 columns (of the gated
 // block: 128 of the gate and the same 128 of the up-projection); each holds 128
 // tokens' rows and half of the weight rows.  Persistent pairs walk the tiles;
-// warp 0 loads, warp 1 of the first CTA issues the MMAs of both, warp 2 makes
-// the scales, and eight warps scale and add.
+// warp 0 loads, warp 1 of the first CTA issues the MMAs of both, warps 2 and 3
+// make the scales in turn, and eight warps scale and add.
 //
 // Each block of K gets an accumulator of 256 columns of its own, read while the
 // tensor cores fill the other one.  A thread holds 128 sums: of 128 neighbouring
 // columns (part 0 or 1 of the tile's two blocks of columns) or, gated, of 64 of
 // the gate and the same 64 of the up-projection.
 //
-// The eight warps' way through a block bounds this, not the tensor cores, which
-// take 515 clocks for one (with the loads from TMEM and the additions taken out,
-// in a copy, 8192 x 7168 x 4096 took 142 us, with both 217, now 193): a look at a
-// barrier takes about 80 clocks, an arrival 40, the loads of 64 columns 60 and
-// their additions 70, one after the other, and code that is longer is fetched
-// more slowly (two blocks unrolled: 222 us).  So a block has one wait and one
+// The eight warps' way through a block bounds this, not the tensor cores: a block
+// takes some 970 clocks (471 ns), the tensor cores 515 of them (with the loads from
+// TMEM and the additions taken out, in a copy, 8192 x 7168 x 4096 took 142 us, with
+// both 217, now 192).  By itself a warp takes about 80 clocks for a look at a
+// barrier, 40 for an arrival, 60 for the loads of 64 columns and 70 for their
+// additions, but two warps share a scheduler: with clocks read on the way (in a
+// copy, which that slowed to 1280 clocks a block) a block's additions took 480, its
+// loads' waits 120, the release 130, barriers and scales 420 and the rest 120, one
+// after the other.  Code that is longer is fetched more slowly (two blocks
+// unrolled: 222 us).  So a block has one wait and one
 // arrival, scales come for four blocks at a time from two warps of their own, the
 // next loads are under way while columns are added, and the next block's barrier
 // is looked at meanwhile.  Tried and not kept: accumulators of 128 columns, four

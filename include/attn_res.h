@@ -522,8 +522,8 @@ attn_res_status_t attn_res_f8_dequantize(const attn_res_f8_t* q, attn_res_bf16_t
  * 128 columns the codes' products are summed on the tensor cores (tcgen05, fp32)
  * and then multiplied by the fp32 product of the two scales; the blocks' sums
  * are added in fp32, and the result is rounded once.  (A product of scales below
- * 2^-126 has fewer bits, one above 2^128 is infinite.)  Repeated calls give the
- * same bits.
+ * 2^-126 has fewer bits and is 0 below 2^-149; one above 2^128 is infinite, and
+ * NaN comes of it where a block's sum is 0.)  Repeated calls give the same bits.
  *
  * out_type: ATTN_RES_OUT_BF16, ATTN_RES_OUT_F32, or ATTN_RES_OUT_F32_ADD, which
  * adds to the fp32 rows that are there.  fp32 rows: 16-byte aligned, out_row a
